@@ -113,6 +113,42 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, const int64_t* slot
                                const pa_cache* cache, pa_stream stream);
 
 /*
+ * KV append with rotary positions: pa_reshape_and_cache of k rotated by its
+ * position and of v as it is, and the rotated q for the attention that
+ * follows, in one pass.
+ *   (a', b') = (a cos - b sin, b cos + a sin)
+ * for the pairs (a, b) of each q and k head's first rotary_dim dims; the dims
+ * from rotary_dim on stay as they are.
+ *
+ *   q              device, rows [num_tokens][num_q_heads][head_dim], or NULL (with
+ *                  q_out NULL): k and v alone.
+ *   k, v           device, rows [num_tokens][num_kv_heads][head_dim].
+ *   *_stride       elements from one token's row to the next, at least heads *
+ *                  head_dim, a multiple of 16 bytes: q, k and v may be views of
+ *                  one projection's rows. All in the cache dtype, bf16 for an
+ *                  8-bit cache.
+ *   positions      device int32 [num_tokens]. A position outside [0,
+ *                  max_positions) leaves the token out (nothing of it is
+ *                  written) and is recorded as PA_ERR_DEVICE_BOUNDS.
+ *   cos_sin        device fp32 [max_positions][rotary_dim], 16-byte aligned:
+ *                  rotary_dim / 2 cosines, then as many sines, of pair 0, 1, ...
+ *                  at that position.
+ *   rotary_dim     a multiple of 16, 16 .. head_dim.
+ *   interleaved    0: pair i is dims (i, i + rotary_dim / 2); 1: dims (2i, 2i + 1).
+ *   slot_mapping   as for pa_reshape_and_cache; a token whose slot is -1 (or out
+ *                  of range) still has its q rotated.
+ *   q_out          device [num_tokens][num_q_heads][head_dim], contiguous, q's
+ *                  type. q_out == q is allowed when q_stride is num_q_heads *
+ *                  head_dim; any other overlap of an output with an input is not.
+ * The rotation is computed in fp32, each operation rounded, and rounded once to
+ * the stored type (for an 8-bit cache the rotated fp32 value is quantised).
+ */
+pa_status pa_rotate_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* positions, const float* cos_sin, int32_t max_positions,
+                              int32_t rotary_dim, int32_t interleaved, const int64_t* slot_mapping, int32_t num_tokens,
+                              int32_t num_q_heads, const pa_cache* cache, void* q_out, pa_stream stream);
+
+/*
  * Copy whole physical blocks, K and V: cache[dst] = cache[src] for each pair.
  * P2 §3.4: before a write into a block shared by several sequences, the block
  * is copied and the writer's table is pointed at the copy (copy-on-write).

@@ -34,6 +34,9 @@ Modules and what pins each one (tests/test_oracle_*.py):
                  a copy-on-write split inside the prefix, lone sequences,
                  group-size cuts, the alignment cut) in
                  tests/test_oracle_prefix_groups.py.
+  rotary         rotary positions of q and k. Pinned by norms, by the dot
+                 product of two rotated rows depending on their distance alone,
+                 and by complex multiplication (tests/test_oracle_rotary.py).
   replay         replays an operation script (paged_kv_cache_361_b200.workloads)
                  on the oracle's block manager and a contiguous per-sequence
                  history (the "traditional" layout of P1 and P2 §1.2).

@@ -49,6 +49,8 @@ _SIGS = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
     "pa_version": (_I32, []),
     "pa_reshape_and_cache": (_I32, [_VP, _VP, _VP, _I32, _PCACHE, _VP]),
+    "pa_rotate_and_cache": (_I32, [_VP, _I64, _VP, _I64, _VP, _I64, _VP, _VP, _I32, _I32, _I32, _VP, _I32, _I32,
+                                   _PCACHE, _VP, _VP]),
     "pa_copy_blocks": (_I32, [_PCACHE, _VP, _I32, _VP]),
     "pa_decode": (_I32, [_VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _F, _VP, _I32, _VP, _SZ, _VP]),
     "pa_decode_ordered": (_I32, [_VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _VP, _F, _VP, _I32, _VP, _SZ, _VP]),
@@ -169,6 +171,73 @@ def pa_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
         raise ValueError("slot_mapping must be [num_tokens]")
     _check(_lib().pa_reshape_and_cache(k.data_ptr(), v.data_ptr(), _dev(slot_mapping, "slot_mapping", torch.int64),
                                        n, ctypes.byref(c), _stream(k_cache, stream)), "pa_reshape_and_cache")
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, heads_dim=None) -> int:
+    """Elements from one token's [heads][head_dim] row to the next, for a tensor
+    whose rows are contiguous (a view of a wider projection's rows, say)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3 or (heads_dim is not None and tuple(t.shape[1:]) != heads_dim):
+        raise ValueError(f"{name} must be [num_tokens][heads][head_dim], got {tuple(t.shape)}")
+    n, h, d = t.shape
+    if n == 0 or h == 0:
+        return h * d
+    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: each token's heads must be contiguous")
+    # torch leaves a single row's stride open: it is never walked
+    stride = t.stride(0) if n > 1 else h * d
+    if stride < h * d:
+        raise ValueError(f"{name}: the tokens' rows overlap")
+    return stride
+
+
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, the cache on {first.device}")
+
+
+def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved=False,
+                        stream=None):
+    """Rotates q and k by their positions (int32) and cos_sin, fp32
+    [max_positions][rotary_dim] (see rotary_table), writes k and v to their
+    slots and q to q_out. q, k, v: [num_tokens][heads][head_dim], also as views
+    of one projection's rows; q and q_out may be None."""
+    c = make_cache(k_cache, v_cache)
+    dt, kv = input_dtype(k_cache.dtype), (c.num_kv_heads, c.head_dim)
+    sk, sv = _token_rows(k, "k", dt, kv), _token_rows(v, "v", dt, kv)
+    n = int(k.shape[0])
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    sq = hq = 0
+    if q is not None:
+        sq, hq = _token_rows(q, "q", dt), int(q.shape[1])
+        _dev(q_out, "q_out", dt, 3)
+        if tuple(q.shape) != (n, hq, c.head_dim) or q_out.shape != q.shape:
+            raise ValueError("q, q_out must be [num_tokens][num_q_heads][head_dim]")
+    _dev(cos_sin, "cos_sin", torch.float32, 2)
+    if int(v.shape[0]) != n or tuple(positions.shape) != (n,) or tuple(slot_mapping.shape) != (n,):
+        raise ValueError("v, positions and slot_mapping must have a row for every token of k")
+    _same_device(k_cache, v_cache=v_cache, q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
+                 slot_mapping=slot_mapping, q_out=q_out)
+    with torch.cuda.device(k_cache.device):
+        _check(_lib().pa_rotate_and_cache(q.data_ptr() if q is not None else None, sq, k.data_ptr(), sk, v.data_ptr(),
+                                          sv, _dev(positions, "positions", torch.int32), cos_sin.data_ptr(),
+                                          int(cos_sin.shape[0]), int(cos_sin.shape[1]), 1 if interleaved else 0,
+                                          _dev(slot_mapping, "slot_mapping", torch.int64), n, hq, ctypes.byref(c),
+                                          q_out.data_ptr() if q is not None else None, _stream(k_cache, stream)),
+               "pa_rotate_and_cache")
+
+
+def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
+    """cos_sin of pa_rotate_and_cache for the angles position * base^(-2i / rotary_dim),
+    computed in 64 bits (a 32-bit product is 4e-3 off at position 10^5)."""
+    inv = float(base) ** (-torch.arange(0, rotary_dim, 2, dtype=torch.float64, device=device) / rotary_dim)
+    angle = torch.outer(torch.arange(max_positions, dtype=torch.float64, device=device), inv)
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
 def pa_copy_blocks(k_cache, v_cache, src_dst_pairs, stream=None):

@@ -10,6 +10,7 @@ P1 = "Paged Attention：大模型推理显存优化的核心方案", P2 = "Paged
   add_sequence  prefill write (P2 §3.2.1)
   fork          prefix sharing (P1 "跨请求的内存共享", P2 §3.4)
   append        decode-step write with copy-on-write (P2 §3.2.2 steps 1-3, §3.4)
+  append_rotated  the same for any number of tokens, rotary positions applied on the way
   decode        attention over the block tables (P2 §3.2.2 step 4, §4.1)
   free          return blocks to the pool (P2 §3.3)
 """
@@ -114,6 +115,57 @@ class PagedKVCache:
             B.pa_copy_blocks(self.k_cache, self.v_cache, self._pairs.upload(pairs))
         B.pa_reshape_and_cache(k, v, self._slots.upload(slots), self.k_cache, self.v_cache)
         return slots, pairs
+
+    def _extend(self, seq_ids, counts) -> np.ndarray:
+        """Slots of counts[i] new tokens for each sequence seq_ids[i] (a new
+        sequence is created; a live one grows, its shared last block copied
+        first), all or nothing."""
+        if len(set(seq_ids)) != len(seq_ids):
+            raise ValueError("seq_ids must be distinct")
+        if len(counts) != len(seq_ids) or min(counts, default=0) < 0:
+            raise ValueError("counts must give a number of tokens for every sequence")
+        slots, made = {}, []
+        try:
+            for s, n in zip(seq_ids, counts):
+                if s not in self.lens:
+                    slots[s] = self.bm.add_seq(s, n)
+                    made.append(s)
+            live = [s for s, n in zip(seq_ids, counts) if s in self.lens for _ in range(n)]
+            grown, pairs = self.bm.append_slots(live)
+        except B.PagedAttnError:
+            for s in made:
+                self.bm.free_seq(s)
+            raise
+        if len(pairs):
+            B.pa_copy_blocks(self.k_cache, self.v_cache, self._pairs.upload(pairs))
+        at = 0
+        for s, n in zip(seq_ids, counts):
+            if s in self.lens:
+                slots[s] = grown[at:at + n]
+                at += n
+            self.lens[s] = self.lens.get(s, 0) + n
+        return np.concatenate([slots[s] for s in seq_ids]) if len(seq_ids) else np.empty(0, np.int64)
+
+    def append_rotated(self, seq_ids, counts, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
+                       interleaved: bool = False) -> torch.Tensor:
+        """counts[i] new tokens for each sequence (new or live), their rows in q,
+        k, v back to back (views of one projection's rows will do): q and k are
+        rotated by the tokens' positions (pa_rotate_and_cache, cos_sin from
+        rotary_table), k and v written; returns the rotated q [T][Hq][D] for
+        decode, decode_multi or prefill_window."""
+        counts = [int(c) for c in counts]
+        if sum(counts) != int(k.shape[0]):
+            raise ValueError("counts must give every sequence its rows of k")
+        first = [self.lens.get(s, 0) for s in seq_ids]
+        if max((f + c for f, c in zip(first, counts)), default=0) > cos_sin.shape[0]:
+            raise ValueError("a sequence outgrew the rotary table")
+        slots = self._extend(seq_ids, counts)
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        if len(slots):
+            pos = np.concatenate([np.arange(f, f + c, dtype=np.int32) for f, c in zip(first, counts)])
+            B.pa_rotate_and_cache(q, k, v, self._lens.upload(pos), cos_sin, self._slots.upload(slots), self.k_cache,
+                                  self.v_cache, q_out, interleaved)
+        return q_out
 
     def enable_swap(self, num_host_blocks: int):
         """Allocate a pinned host pool of num_host_blocks blocks (same layout)."""

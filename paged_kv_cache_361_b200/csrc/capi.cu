@@ -15,6 +15,7 @@
 #include "decode_simt.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"
+#include "rotary.cuh"
 
 namespace {
 
@@ -430,6 +431,67 @@ pa_status pa_reshape_and_cache(const void* k, const void* v, const int64_t* slot
       static_cast<const int4*>(k), static_cast<const int4*>(v), slot_mapping, static_cast<int4*>(cache->k),
       static_cast<int4*>(cache->v), num_tokens, cache->num_kv_heads, cache->block_size, row_chunks,
       cache->num_blocks * cache->block_size);
+  return launched();
+}
+
+pa_status pa_rotate_and_cache(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* positions, const float* cos_sin, int32_t max_positions,
+                              int32_t rotary_dim, int32_t interleaved, const int64_t* slot_mapping, int32_t num_tokens,
+                              int32_t num_q_heads, const pa_cache* cache, void* q_out, pa_stream stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  const int32_t D = cache->head_dim, hkv = cache->num_kv_heads;
+  if (num_tokens < 0 || max_positions <= 0 || num_q_heads < 0 || (interleaved != 0 && interleaved != 1))
+    return PA_ERR_INVALID_ARG;
+  if (rotary_dim < 16 || rotary_dim > D || rotary_dim % 16) return PA_ERR_UNSUPPORTED;
+  if ((q == nullptr) != (q_out == nullptr) || (q && num_q_heads == 0)) return PA_ERR_INVALID_ARG;
+  const int32_t hq = q ? num_q_heads : 0;
+  const int64_t es = cache->dtype == PA_F32 ? 4 : 2;
+  const int64_t heads = static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(hkv);
+  if (heads * (D / 16) > INT32_MAX / 4096) return PA_ERR_UNSUPPORTED;
+  if ((q && (q_stride < static_cast<int64_t>(hq) * D || q_stride * es % 16)) ||
+      k_stride < static_cast<int64_t>(hkv) * D || k_stride * es % 16 || v_stride < static_cast<int64_t>(hkv) * D ||
+      v_stride * es % 16)
+    return PA_ERR_INVALID_ARG;
+  if (q && q_out == q && q_stride != static_cast<int64_t>(hq) * D) return PA_ERR_INVALID_ARG;
+  if (num_tokens == 0) return PA_OK;
+  if (!k || !v || !positions || !cos_sin || !slot_mapping || !aligned16(q) || !aligned16(q_out) || !aligned16(k) ||
+      !aligned16(v) || !aligned16(cos_sin) || (reinterpret_cast<uintptr_t>(positions) & 3) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7))
+    return PA_ERR_INVALID_ARG;
+  RotateArgs a;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.slots = slot_mapping;
+  a.q_out = q_out;
+  a.kc = cache->k;
+  a.vc = cache->v;
+  a.num_slots = cache->num_blocks * cache->block_size;
+  a.num_tokens = num_tokens;
+  a.max_positions = max_positions;
+  a.rd = rotary_dim;
+  a.interleaved = interleaved;
+  a.hq = hq;
+  a.hkv = hkv;
+  a.bs = cache->block_size;
+  a.dshift = D == 128 ? 3 : 2;
+  a.units = static_cast<int32_t>(heads * (D / 16));
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  const int threads = 256;
+  a.tokens_per_cta = a.units >= threads ? 1 : threads / a.units;
+  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(num_tokens) + a.tokens_per_cta - 1) / a.tokens_per_cta);
+  auto kern = cache->dtype == PA_F32      ? rotate_and_cache_kernel<float, 0>
+              : cache->dtype == PA_BF16   ? rotate_and_cache_kernel<__nv_bfloat16, 0>
+              : cache->dtype == PA_INT8   ? rotate_and_cache_kernel<__nv_bfloat16, kCodeS8>
+                                          : rotate_and_cache_kernel<__nv_bfloat16, kCodeE4M3>;
+  kern<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
 
