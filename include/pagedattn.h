@@ -363,6 +363,73 @@ pa_status pa_decode_cascade(const void* q, int32_t num_seqs, int32_t num_q_heads
                             const int32_t* seq_order, float scale, float* out, void* workspace,
                             size_t workspace_bytes, pa_stream stream);
 
+/*
+ * What turns scores into weights, beyond causality, in pa_decode_multi and
+ * pa_prefill_window. For the new token at position p and query head h:
+ *   x_j = scale * q.k_j                            (softcap 0)
+ *   x_j = softcap * tanh(scale * q.k_j / softcap)  (softcap > 0)
+ *   keys j with p - window < j <= p                (window 0: every j <= p)
+ *   den = sum_j exp(x_j) + exp(sinks[h]);  out = sum_j exp(x_j) v_j / den;  lse = log(den)
+ */
+typedef struct {
+  int32_t window;      /* >= 0 */
+  float softcap;       /* >= 0, finite */
+  const float* sinks;  /* device fp32 [num_q_heads], finite or -inf; NULL: no sink */
+  float* lse;          /* device fp32 [num_tokens][num_q_heads], written; NULL: not wanted */
+} pa_attn_options;
+
+/* New tokens per sequence that pa_decode_multi takes at most. */
+#define PA_DECODE_MULTI_MAX_TOKENS 16
+
+/*
+ * Decode attention of one or a few new tokens per sequence (a decode step, or
+ * drafted tokens that are checked in one pass; batches may mix both), split
+ * over the cache's length where that fills the GPU. Every new token attends,
+ * through the block table, to the keys of its window up to and including its
+ * own (already appended), by the rule of `options`.
+ *
+ *   q              device bf16 [num_tokens][num_q_heads][head_dim], the new tokens
+ *                  of all sequences back to back.
+ *   cu_q_lens      device int32 [num_seqs + 1]: sequence s owns rows cu_q_lens[s]
+ *                  .. cu_q_lens[s+1]-1; NULL: one token per sequence, row s.
+ *   max_q_len      host bound on every sequence's count, 1 ..
+ *                  PA_DECODE_MULTI_MAX_TOKENS (1 with cu_q_lens NULL).
+ *   num_tokens     rows of q, out and lse. A count or row outside max_q_len or
+ *                  num_tokens is recorded (PA_ERR_DEVICE_BOUNDS) and cut; rows
+ *                  of no sequence are left as they were.
+ *   context_lens   device int32 [num_seqs]: lengths with the new tokens; new token
+ *                  i of n sits at position L - n + i. L above max_context_len is
+ *                  recorded and clamped; so is n > L with cu_q_lens given. A token
+ *                  that sees no key (a position below 0; L = 0 without cu_q_lens)
+ *                  gets a zero row and lse = its sink, or -inf.
+ *   block_tables   as for pa_decode. Entries of blocks that lie wholly before
+ *                  every window are not used (those blocks may have been freed).
+ *   scale          > 0.
+ *   out            device bf16 [num_tokens][num_q_heads][head_dim].
+ *   partition_tokens  -1: chosen by the library; 0: no split; else a multiple of
+ *                  64: each sequence's keys, from the 64-key boundary at or before
+ *                  the first one seen, in partitions of that many.
+ *   workspace      >= pa_decode_multi_workspace_bytes(...) bytes, 256-byte aligned;
+ *                  may be NULL where that is 0. Its contents need no initial value.
+ * q, out and workspace 16-byte aligned. Accumulation is fp32; the result is
+ * rounded once to bf16. Over an 8-bit cache q and the weights enter the products
+ * as f16. Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
+ * 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}, max_context_len up to
+ * 2^30. Calls sharing a workspace must not overlap on the GPU. options may be
+ * NULL: plain causal attention.
+ */
+pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
+                          int32_t max_q_len, int32_t num_q_heads, const pa_cache* cache, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
+                          float scale, const pa_attn_options* options, void* out, int32_t partition_tokens,
+                          void* workspace, size_t workspace_bytes, pa_stream stream);
+
+/* Workspace bytes of pa_decode_multi for these sizes (0 where it does not
+ * split). window as in pa_attn_options; partition_tokens may be -1. */
+size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                                       int32_t window, int32_t partition_tokens);
+
 size_t pa_decode_cascade_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_context_len, int32_t block_size, int32_t max_prefix_tokens);
 

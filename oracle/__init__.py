@@ -34,6 +34,10 @@ Modules and what pins each one (tests/test_oracle_*.py):
                  a copy-on-write split inside the prefix, lone sequences,
                  group-size cuts, the alignment cut) in
                  tests/test_oracle_prefix_groups.py.
+  options        attention with a sliding window, capped scores, sinks and the
+                 log-sum-exp. Pinned by the plain oracle where all are off, by a
+                 masked matrix form, and by closed forms
+                 (tests/test_oracle_options.py).
   rotary         rotary positions of q and k. Pinned by norms, by the dot
                  product of two rotated rows depending on their distance alone,
                  and by complex multiplication (tests/test_oracle_rotary.py).

@@ -40,10 +40,15 @@ class pa_cache(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("k_scale", ctypes.c_float), ("v_scale", ctypes.c_float)]
 
 
+class pa_attn_options(ctypes.Structure):
+    _fields_ = [("window", ctypes.c_int32), ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
+                ("lse", ctypes.c_void_p)]
+
+
 _L = None
 _VP, _I32, _I64, _SZ, _F = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 _P32, _P64 = ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(ctypes.c_int64)
-_PCACHE = ctypes.POINTER(pa_cache)
+_PCACHE, _POPT = ctypes.POINTER(pa_cache), ctypes.POINTER(pa_attn_options)
 
 _SIGS = {
     "pa_status_string": (ctypes.c_char_p, [_I32]),
@@ -56,6 +61,9 @@ _SIGS = {
     "pa_decode_ordered": (_I32, [_VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _VP, _F, _VP, _I32, _VP, _SZ, _VP]),
     "pa_decode_append": (_I32, [_VP, _VP, _VP, _VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _VP, _F, _VP, _I32, _VP,
                                 _SZ, _VP]),
+    "pa_decode_multi": (_I32, [_VP, _I32, _I32, _VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _F, _POPT, _VP, _I32,
+                               _VP, _SZ, _VP]),
+    "pa_decode_multi_workspace_bytes": (_SZ, [_I32] * 9),
     "pa_decode_partition_tokens": (_I32, [_I32, _I32, _I32, _I32, _I32]),
     "pa_decode_ordered_partition_tokens": (_I32, [_I32, _I32, _I32, _I32, _I32]),
     "pa_decode_cascade": (_I32, [_VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I32,
@@ -348,6 +356,65 @@ def pa_prefill(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale
     _check(_lib().pa_prefill(q.data_ptr(), B, cu_q_lens.data_ptr(), int(max_q_len), hq, ctypes.byref(c),
                              block_tables.data_ptr(), int(block_tables.shape[1]), context_lens.data_ptr(),
                              int(max_context_len), float(scale), out.data_ptr(), _stream(q, stream)), "pa_prefill")
+
+
+def _attn_options(window, softcap, sinks, lse, num_tokens, num_q_heads) -> pa_attn_options:
+    if sinks is not None:
+        _dev(sinks, "sinks", torch.float32, 1)
+        if tuple(sinks.shape) != (num_q_heads,):
+            raise ValueError("sinks must be [num_q_heads]")
+    if lse is not None:
+        _dev(lse, "lse", torch.float32, 2)
+        if tuple(lse.shape) != (num_tokens, num_q_heads):
+            raise ValueError("lse must be [num_tokens][num_q_heads]")
+    return pa_attn_options(int(window), float(softcap), sinks.data_ptr() if sinks is not None else None,
+                           lse.data_ptr() if lse is not None else None)
+
+
+def pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
+                                    max_context_len, window=0, partition_tokens=-1) -> int:
+    return int(_lib().pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads,
+                                                      head_dim, max_context_len, window, partition_tokens))
+
+
+def _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, **others):
+    """Checks of attention over packed new tokens; (pa_cache, T, Hq, num_seqs)."""
+    c = make_cache(k_cache, v_cache)
+    _dev(q, "q", input_dtype(k_cache.dtype), 3)
+    _dev(out, "out", q.dtype, 3)
+    T, hq, d = q.shape
+    if d != c.head_dim or out.shape != q.shape:
+        raise ValueError("q/out shape mismatch")
+    _dev(block_tables, "block_tables", torch.int32, 2)
+    _dev(context_lens, "context_lens", torch.int32, 1)
+    n = int(context_lens.shape[0])
+    if block_tables.shape[0] != n:
+        raise ValueError("block_tables must have num_seqs rows")
+    if cu_q_lens is not None:
+        _dev(cu_q_lens, "cu_q_lens", torch.int32, 1)
+        if cu_q_lens.shape[0] != n + 1:
+            raise ValueError("cu_q_lens must have num_seqs + 1 entries")
+    _same_device(k_cache, v_cache=v_cache, q=q, out=out, cu_q_lens=cu_q_lens, block_tables=block_tables,
+                 context_lens=context_lens, **others)
+    return c, int(T), int(hq), n
+
+
+def pa_decode_multi(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale, out, max_q_len, max_context_len,
+                    window=0, softcap=0.0, sinks=None, lse=None, partition_tokens=-1, workspace=None, stream=None):
+    """Attention of one or a few new tokens per sequence (rows of q [T][Hq][D] by
+    cu_q_lens, or with None one row per sequence) over the paged cache; out has
+    q's type, lse (optional) fp32 [T][Hq]. See pagedattn.h."""
+    c, T, hq, n = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, sinks=sinks, lse=lse,
+                               workspace=workspace)
+    opt = _attn_options(window, softcap, sinks, lse, T, hq)
+    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_dev(workspace, "workspace"),
+                                                            workspace.numel() * workspace.element_size())
+    with torch.cuda.device(k_cache.device):
+        _check(_lib().pa_decode_multi(q.data_ptr(), T, n, cu_q_lens.data_ptr() if cu_q_lens is not None else None,
+                                      int(max_q_len), hq, ctypes.byref(c), block_tables.data_ptr(),
+                                      int(block_tables.shape[1]), context_lens.data_ptr(), int(max_context_len),
+                                      float(scale), ctypes.byref(opt), out.data_ptr(), int(partition_tokens), ws_ptr,
+                                      ws_bytes, _stream(k_cache, stream)), "pa_decode_multi")
 
 
 def pa_decode_cascade_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size,

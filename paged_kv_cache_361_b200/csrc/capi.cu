@@ -12,6 +12,7 @@
 #include "cache_ops.cuh"
 #include "decode_f8.cuh"
 #include "decode_mma.cuh"
+#include "decode_multi.cuh"
 #include "decode_simt.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"
@@ -385,6 +386,69 @@ pa_status launch_reduce(const DecodeArgs& a, cudaStream_t st) {
   return launched();
 }
 
+// pa_decode_multi: groups of 8 rows a CTA handles at once.
+int multi_groups(int32_t max_q_len, int32_t G) {
+  const int32_t rows = max_q_len * G;
+  return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
+}
+
+// Its partitions. Returns their size (a multiple of 64, INT32_MAX: no split)
+// and how many the longest sequence has.
+int32_t multi_partition(int32_t num_seqs, int32_t max_q_len, int32_t hq, int32_t hkv, int32_t max_ctx, int32_t window,
+                        int32_t requested, int32_t* parts, int32_t* row_tiles) {
+  const int32_t G = hq / hkv, ng = multi_groups(max_q_len, G);
+  *row_tiles = (max_q_len * G + 8 * ng - 1) / (8 * ng);
+  int64_t span = max_ctx;
+  if (window > 0 && static_cast<int64_t>(window) + max_q_len - 1 < span) span = window + max_q_len - 1;
+  span += 63;  // the first key, down to a multiple of 64
+  int64_t P = requested;
+  if (requested < 0) {
+    const int64_t units = static_cast<int64_t>(num_seqs) * hkv * *row_tiles;
+    const int64_t slots = 148 * (ng == 4 ? 2 : 3);
+    const int64_t want = (2 * slots + units - 1) / units;
+    P = ((span + want - 1) / want + 63) / 64 * 64;
+    if (P < 256) P = 256;
+  }
+  if (P <= 0 || P >= span) {
+    *parts = 1;
+    return INT32_MAX;
+  }
+  *parts = static_cast<int32_t>((span + P - 1) / P);
+  return static_cast<int32_t>(P);
+}
+
+// The options of pa_decode_multi and pa_prefill_window.
+pa_status check_options(const pa_attn_options* o) {
+  if (!o) return PA_OK;
+  if (o->window < 0 || !std::isfinite(o->softcap) || o->softcap < 0.f) return PA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(o->sinks) & 3) || (reinterpret_cast<uintptr_t>(o->lse) & 3))
+    return PA_ERR_INVALID_ARG;
+  return PA_OK;
+}
+
+constexpr int32_t kMaxOptionContext = 1 << 30;  // positions minus windows stay within 32 bits
+
+template <int D, int NG, int CF>
+pa_status launch_multi(const MultiArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  using Cfg = MultiCfg<D, NG, CF>;
+  auto kern = decode_multi_kernel<D, NG, CF>;
+  if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, true)) return PA_ERR_CUDA;
+  kern<<<dim3(a.hkv, a.num_seqs, a.max_parts * a.row_tiles), Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, a);
+  const pa_status r = launched();
+  if (r != PA_OK || a.max_parts == 1) return r;
+  const unsigned rows = static_cast<unsigned>((a.max_q * a.hq + kMultiMergeWarps - 1) / kMultiMergeWarps);
+  return launch_kernel(decode_multi_merge_kernel<D>, dim3(rows, a.num_seqs), dim3(32 * kMultiMergeWarps), 0, st, true, a);
+}
+
+template <int D, int CF>
+pa_status dispatch_multi(const MultiArgs& a, int ng, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  switch (ng) {
+    case 1: return launch_multi<D, 1, CF>(a, tk, tv, st);
+    case 2: return launch_multi<D, 2, CF>(a, tk, tv, st);
+    default: return launch_multi<D, 4, CF>(a, tk, tv, st);
+  }
+}
+
 }  // namespace
 
 extern "C" {
@@ -705,6 +769,105 @@ pa_status pa_prefill(const void* q, int32_t num_seqs, const int32_t* cu_q_lens, 
     case 4: return launch(prefill_tc_kernel<64, 4, 1>, C64::kThreads, C64::kSmemBytes);
     default: return launch(prefill_tc_kernel<64, 8, 1>, C64::kThreads, C64::kSmemBytes);
   }
+}
+
+size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
+                                       int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
+                                       int32_t window, int32_t partition_tokens) {
+  if (num_tokens <= 0 || num_seqs <= 0 || max_q_len <= 0 || max_q_len > PA_DECODE_MULTI_MAX_TOKENS ||
+      num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 8 ||
+      head_dim <= 0 || max_context_len < 0 || max_context_len > kMaxOptionContext || window < 0 || partition_tokens < -1)
+    return 0;
+  int32_t parts, row_tiles;
+  multi_partition(num_seqs, max_q_len, num_q_heads, num_kv_heads, max_context_len, window, partition_tokens, &parts,
+                  &row_tiles);
+  if (parts == 1) return 0;
+  return ml_bytes(num_tokens, num_q_heads, parts) + static_cast<size_t>(num_tokens) * num_q_heads * parts * head_dim * 4;
+}
+
+pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
+                          int32_t max_q_len, int32_t num_q_heads, const pa_cache* cache, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* context_lens, int32_t max_context_len,
+                          float scale, const pa_attn_options* options, void* out, int32_t partition_tokens,
+                          void* workspace, size_t workspace_bytes, pa_stream stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if ((st = check_options(options)) != PA_OK) return st;
+  if (num_tokens < 0 || num_seqs < 0 || max_q_len <= 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
+      max_context_len < 0 || partition_tokens < -1 || (partition_tokens > 0 && partition_tokens % 64))
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % cache->num_kv_heads) return PA_ERR_INVALID_ARG;
+  const int G = num_q_heads / cache->num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
+  const bool f8 = is_8bit(cache->dtype);
+  if ((cache->dtype != PA_BF16 && !f8) || cache->block_size < 8) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size > INT32_MAX ||
+      max_q_len > PA_DECODE_MULTI_MAX_TOKENS || max_context_len > kMaxOptionContext)
+    return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * cache->block_size)
+    return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.f) return PA_ERR_INVALID_ARG;
+  if (!cu_q_lens && (max_q_len != 1 || num_tokens < num_seqs)) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_tokens == 0) return PA_OK;
+  if (!q || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(cu_q_lens) & 3) || (reinterpret_cast<uintptr_t>(block_tables) & 3) ||
+      (reinterpret_cast<uintptr_t>(context_lens) & 3))
+    return PA_ERR_INVALID_ARG;
+  const int32_t window = options ? options->window : 0;
+  MultiArgs a;
+  int32_t parts, row_tiles;
+  a.part_tokens = multi_partition(num_seqs, max_q_len, num_q_heads, cache->num_kv_heads, max_context_len, window,
+                                  partition_tokens, &parts, &row_tiles);
+  if (num_seqs > 65535 || static_cast<int64_t>(parts) * row_tiles > 65535) return PA_ERR_UNSUPPORTED;
+  const size_t need = pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads,
+                                                      cache->num_kv_heads, cache->head_dim, max_context_len, window,
+                                                      partition_tokens);
+  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+    return PA_ERR_INVALID_ARG;
+  a.q = static_cast<const __nv_bfloat16*>(q);
+  a.cu_q = cu_q_lens;
+  a.tables = block_tables;
+  a.lens = context_lens;
+  a.sinks = options ? options->sinks : nullptr;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = options ? options->lse : nullptr;
+  a.ws_ml = static_cast<float*>(workspace);
+  a.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(num_tokens, num_q_heads, parts));
+  a.num_blocks = cache->num_blocks;
+  a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.max_q = max_q_len;
+  a.hq = num_q_heads;
+  a.hkv = cache->num_kv_heads;
+  a.bs = cache->block_size;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_ctx = max_context_len;
+  a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
+  a.window = window > 0 && window < max_context_len ? window : (max_context_len > 0 ? max_context_len : 1);
+  a.max_parts = parts;
+  a.row_tiles = row_tiles;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
+  a.scale_log2 = scale * kLog2e * ks;
+  a.cap_log2 = cap * kLog2e;
+  a.cap_arg = cap > 0.f ? 2.f * kLog2e * (scale / cap) * ks : 0.f;
+  a.v_scale = f8 ? cache->v_scale : 1.f;
+  const int D = cache->head_dim, ng = multi_groups(max_q_len, G);
+  CUtensorMap tk, tv;
+  const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
+  auto enc = [&](CUtensorMap* m, void* base) {
+    if (f8) return encode_rows_u8(m, base, rows, D, cache->block_size);
+    return D == 128 ? encode_rows_halves(m, base, rows, cache->block_size) : encode_rows(m, base, rows, D, cache->block_size);
+  };
+  if (!enc(&tk, cache->k) || !enc(&tv, cache->v)) return PA_ERR_CUDA;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto by_format = [&](auto d) -> pa_status {
+    constexpr int DD = decltype(d)::value;
+    if (!f8) return dispatch_multi<DD, 0>(a, ng, tk, tv, s);
+    return cache->dtype == PA_INT8 ? dispatch_multi<DD, kCodeS8>(a, ng, tk, tv, s)
+                                   : dispatch_multi<DD, kCodeE4M3>(a, ng, tk, tv, s);
+  };
+  return D == 128 ? by_format(std::integral_constant<int, 128>{}) : by_format(std::integral_constant<int, 64>{});
 }
 
 // Shared-prefix decode: prefix partitions of this many tokens (a multiple of
