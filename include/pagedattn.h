@@ -394,9 +394,10 @@ typedef struct {
  *                  .. cu_q_lens[s+1]-1; NULL: one token per sequence, row s.
  *   max_q_len      host bound on every sequence's count, 1 ..
  *                  PA_DECODE_MULTI_MAX_TOKENS (1 with cu_q_lens NULL).
- *   num_tokens     rows of q, out and lse. A count or row outside max_q_len or
- *                  num_tokens is recorded (PA_ERR_DEVICE_BOUNDS) and cut; rows
- *                  of no sequence are left as they were.
+ *   num_tokens     rows of q, out and lse. A sequence whose rows do not lie in 0 ..
+ *                  num_tokens - 1, or are more than max_q_len, is left out and
+ *                  recorded (PA_ERR_DEVICE_BOUNDS); rows of no sequence are left
+ *                  as they were.
  *   context_lens   device int32 [num_seqs]: lengths with the new tokens; new token
  *                  i of n sits at position L - n + i. L above max_context_len is
  *                  recorded and clamped; so is n > L with cu_q_lens given. A token
@@ -413,7 +414,8 @@ typedef struct {
  *                  may be NULL where that is 0. Its contents need no initial value.
  * q, out and workspace 16-byte aligned. Accumulation is fp32; the result is
  * rounded once to bf16. Over an 8-bit cache q and the weights enter the products
- * as f16. Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
+ * as f16. V must be finite at every key that some new token of its sequence sees
+ * (a weight of 0 does not hide an infinity or NaN there). Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
  * 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}, max_context_len up to
  * 2^30. Calls sharing a workspace must not overlap on the GPU. options may be
  * NULL: plain causal attention.
@@ -429,6 +431,30 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
 size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                                        int32_t window, int32_t partition_tokens);
+
+/*
+ * Causal attention of whole prompts or prompt chunks (pa_prefill) by the rule of
+ * `options`: sliding window, capped scores, sinks, log-sum-exp; keys before a
+ * query tile's window are neither read nor multiplied. Arguments as pa_prefill,
+ * but for:
+ *   num_tokens     rows of q, out and lse. A sequence whose rows do not lie in 0 ..
+ *                  num_tokens - 1, or are more than max_q_len, is left out and
+ *                  recorded (PA_ERR_DEVICE_BOUNDS); rows of no sequence are left
+ *                  as they were.
+ *   scale          > 0.
+ *   options        NULL: plain causal attention.
+ *   out            device bf16 [num_tokens][num_q_heads][head_dim]: rounded once.
+ *   block_tables   entries of blocks that lie wholly before every window are not
+ *                  used (those blocks may have been freed).
+ * max_context_len up to 2^30. V must be finite, and up to 65504 in absolute value,
+ * at every key that some new token of its sequence sees: a weight of 0 does not
+ * hide an infinity or NaN there from the tile's other rows.
+ */
+pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
+                            int32_t max_q_len, int32_t num_q_heads, const pa_cache* cache,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t max_context_len, float scale, const pa_attn_options* options, void* out,
+                            pa_stream stream);
 
 size_t pa_decode_cascade_workspace_bytes(int32_t num_seqs, int32_t num_q_heads, int32_t num_kv_heads, int32_t head_dim,
                                          int32_t max_context_len, int32_t block_size, int32_t max_prefix_tokens);

@@ -41,3 +41,28 @@ def options_attention(q, K, V, scale: float, window: int = 0, cap: float = 0.0, 
                 w = np.exp(x - top) / den
                 out[i, h], size[i, h] = w @ vv, w @ np.abs(vv)
     return out, lse, size
+
+
+def options_attention_masked(q, K, V, scale: float, window: int = 0, cap: float = 0.0, sinks=None):
+    """The same written as one masked matrix softmax per head, for long prompts
+    (an independent form, used to pin the row-wise one too)."""
+    q, K, V = _f64(q), _f64(K), _f64(V)
+    n, hq, d = q.shape
+    L, hkv = K.shape[0], K.shape[1]
+    p, j = np.arange(L - n, L)[:, None], np.arange(L)[None]
+    seen = (j <= p) & (j > p - window) if window else j <= p
+    out, size, lse = np.zeros((n, hq, d)), np.zeros((n, hq, d)), np.empty((n, hq))
+    for h in range(hq):
+        x = scale * q[:, h] @ K[:, h // (hq // hkv)].T
+        x = np.where(seen, cap * np.tanh(x / cap) if cap else x, -np.inf)
+        if sinks is not None:
+            x = np.concatenate([x, np.full((n, 1), float(sinks[h]))], 1)
+        top = x.max(1, keepdims=True, initial=-1e300)
+        e = np.exp(x - top)
+        den = e.sum(1, keepdims=True)
+        with np.errstate(divide="ignore"):
+            lse[:, h] = (np.where(den > 0, top, -np.inf) + np.log(np.where(den > 0, den, 1.0)))[:, 0]
+        w = e[:, :L] / np.where(den > 0, den, 1.0)
+        v = V[:, h // (hq // hkv)]
+        out[:, h], size[:, h] = w @ v, w @ np.abs(v)
+    return out, lse, size

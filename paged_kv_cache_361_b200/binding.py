@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libpagedattn.so")
 PA_OK, PA_ERR_INVALID_ARG, PA_ERR_UNSUPPORTED, PA_ERR_NO_FREE_BLOCKS, PA_ERR_UNKNOWN_SEQ, PA_ERR_SEQ_EXISTS, \
     PA_ERR_CUDA, PA_ERR_DEVICE_BOUNDS, PA_ERR_DEVICE_TIMEOUT = range(9)
 PA_F32, PA_BF16, PA_FP8_E4M3, PA_INT8 = 0, 1, 2, 3
+PA_DECODE_MULTI_MAX_TOKENS = 16
 _DTYPE = {torch.float32: PA_F32, torch.bfloat16: PA_BF16, torch.float8_e4m3fn: PA_FP8_E4M3, torch.int8: PA_INT8}
 CODED_DTYPES = (torch.float8_e4m3fn, torch.int8)   # 8-bit caches: codes times a per-tensor scale
 
@@ -64,6 +65,7 @@ _SIGS = {
     "pa_decode_multi": (_I32, [_VP, _I32, _I32, _VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _F, _POPT, _VP, _I32,
                                _VP, _SZ, _VP]),
     "pa_decode_multi_workspace_bytes": (_SZ, [_I32] * 9),
+    "pa_prefill_window": (_I32, [_VP, _I32, _I32, _VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _F, _POPT, _VP, _VP]),
     "pa_decode_partition_tokens": (_I32, [_I32, _I32, _I32, _I32, _I32]),
     "pa_decode_ordered_partition_tokens": (_I32, [_I32, _I32, _I32, _I32, _I32]),
     "pa_decode_cascade": (_I32, [_VP, _I32, _I32, _PCACHE, _VP, _I32, _VP, _I32, _I32, _VP, _VP, _VP, _VP, _I32, _I32,
@@ -415,6 +417,22 @@ def pa_decode_multi(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, 
                                       int(block_tables.shape[1]), context_lens.data_ptr(), int(max_context_len),
                                       float(scale), ctypes.byref(opt), out.data_ptr(), int(partition_tokens), ws_ptr,
                                       ws_bytes, _stream(k_cache, stream)), "pa_decode_multi")
+
+
+def pa_prefill_window(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale, out, max_q_len,
+                      max_context_len, window=0, softcap=0.0, sinks=None, lse=None, stream=None):
+    """Causal attention of prompts or prompt chunks (rows of q [T][Hq][D] by
+    cu_q_lens) over the paged cache with a sliding window, capped scores, sinks
+    and the log-sum-exp; out has q's type, lse (optional) fp32 [T][Hq]."""
+    if cu_q_lens is None:
+        raise ValueError("cu_q_lens is needed")
+    c, T, hq, n = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, sinks=sinks, lse=lse)
+    opt = _attn_options(window, softcap, sinks, lse, T, hq)
+    with torch.cuda.device(k_cache.device):
+        _check(_lib().pa_prefill_window(q.data_ptr(), T, n, cu_q_lens.data_ptr(), int(max_q_len), hq, ctypes.byref(c),
+                                        block_tables.data_ptr(), int(block_tables.shape[1]), context_lens.data_ptr(),
+                                        int(max_context_len), float(scale), ctypes.byref(opt), out.data_ptr(),
+                                        _stream(k_cache, stream)), "pa_prefill_window")
 
 
 def pa_decode_cascade_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size,

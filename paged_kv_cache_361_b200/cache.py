@@ -12,6 +12,7 @@ P1 = "Paged Attention：大模型推理显存优化的核心方案", P2 = "Paged
   append        decode-step write with copy-on-write (P2 §3.2.2 steps 1-3, §3.4)
   append_rotated  the same for any number of tokens, rotary positions applied on the way
   decode        attention over the block tables (P2 §3.2.2 step 4, §4.1)
+  attend        the same for any number of new tokens, with a window, capped scores and sinks
   free          return blocks to the pool (P2 §3.3)
 """
 from __future__ import annotations
@@ -152,7 +153,7 @@ class PagedKVCache:
         k, v back to back (views of one projection's rows will do): q and k are
         rotated by the tokens' positions (pa_rotate_and_cache, cos_sin from
         rotary_table), k and v written; returns the rotated q [T][Hq][D] for
-        decode, decode_multi or prefill_window."""
+        decode or attend."""
         counts = [int(c) for c in counts]
         if sum(counts) != int(k.shape[0]):
             raise ValueError("counts must give every sequence its rows of k")
@@ -260,6 +261,41 @@ class PagedKVCache:
             out = torch.empty((T, hq, d), dtype=torch.float32, device=self.device)
         B.pa_prefill(q, self._lens.upload(cu), self.k_cache, self.v_cache, self._tables.upload(tables),
                      self._lens.upload(lens), scale, out, max(counts, default=0), max_len)
+        return out
+
+    def attend(self, seq_ids, counts, q: torch.Tensor, scale: float | None = None, window: int = 0,
+               softcap: float = 0.0, sinks: torch.Tensor | None = None, out: torch.Tensor | None = None,
+               lse: torch.Tensor | None = None) -> torch.Tensor:
+        """Attention of the last counts[i] tokens of each sequence (already
+        appended, append_rotated say), their queries in q [T][Hq][D] back to
+        back, with a sliding window, capped scores and sinks (pa_attn_options):
+        pa_decode_multi while no sequence has more than
+        PA_DECODE_MULTI_MAX_TOKENS of them, pa_prefill_window otherwise. Returns
+        out, of q's type; lse (fp32 [T][Hq]) is written if given."""
+        counts = [int(c) for c in counts]
+        T, hq, d = q.shape
+        if len(counts) != len(seq_ids) or sum(counts) != T:
+            raise ValueError("counts must give every sequence its rows of q")
+        if any(c < 0 or c > self.lens[s] for s, c in zip(seq_ids, counts)):
+            raise ValueError("more new tokens than the sequence has")
+        if scale is None:
+            scale = 1.0 / math.sqrt(d)
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        if T == 0:
+            return out
+        tables, lens, max_len = self.decode_inputs(seq_ids)
+        cu = np.zeros(len(counts) + 1, dtype=np.int32)
+        cu[1:] = np.cumsum(counts)
+        args = (q, self._lens.upload(cu), self.k_cache, self.v_cache, self._tables.upload(tables),
+                self._lens.upload(lens), scale, out, max(counts), max_len)
+        rule = dict(window=window, softcap=softcap, sinks=sinks, lse=lse)
+        if max(counts) > B.PA_DECODE_MULTI_MAX_TOKENS:
+            B.pa_prefill_window(*args, **rule)
+            return out
+        nbytes = B.pa_decode_multi_workspace_bytes(T, len(counts), max(counts), hq, self.k_cache.shape[1], d, max_len,
+                                                   window)
+        B.pa_decode_multi(*args, workspace=self.workspace(nbytes), **rule)
         return out
 
     def shared_prefix_groups(self, seq_ids, group_rows: int):

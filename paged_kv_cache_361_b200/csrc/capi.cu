@@ -449,6 +449,20 @@ pa_status dispatch_multi(const MultiArgs& a, int ng, const CUtensorMap& tk, cons
   }
 }
 
+// pa_prefill_window: the prefill kernel with the score rule.
+template <int D, int TILES, int CF>
+pa_status launch_prefill_window(const PrefillArgs& a, int G, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CUtensorMap& tq, cudaStream_t st) {
+  using Cfg = TcCfg<D, TILES, CF != 0>;
+  auto kern = G == 1   ? prefill_tc_kernel<D, 1, TILES, CF, true>
+              : G == 2 ? prefill_tc_kernel<D, 2, TILES, CF, true>
+              : G == 4 ? prefill_tc_kernel<D, 4, TILES, CF, true>
+                       : prefill_tc_kernel<D, 8, TILES, CF, true>;
+  if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, false)) return PA_ERR_CUDA;
+  kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, tq, tq, a);  // (no output map: O goes out through plain stores)
+  return launched();
+}
+
 }  // namespace
 
 extern "C" {
@@ -769,6 +783,83 @@ pa_status pa_prefill(const void* q, int32_t num_seqs, const int32_t* cu_q_lens, 
     case 4: return launch(prefill_tc_kernel<64, 4, 1>, C64::kThreads, C64::kSmemBytes);
     default: return launch(prefill_tc_kernel<64, 8, 1>, C64::kThreads, C64::kSmemBytes);
   }
+}
+
+pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
+                            int32_t max_q_len, int32_t num_q_heads, const pa_cache* cache,
+                            const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* context_lens,
+                            int32_t max_context_len, float scale, const pa_attn_options* options, void* out,
+                            pa_stream stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if ((st = check_options(options)) != PA_OK) return st;
+  if (num_tokens < 0 || num_seqs < 0 || max_q_len < 0 || num_q_heads <= 0 || max_blocks_per_seq <= 0 ||
+      max_context_len < 0)
+    return PA_ERR_INVALID_ARG;
+  if (num_q_heads % cache->num_kv_heads) return PA_ERR_INVALID_ARG;
+  const int G = num_q_heads / cache->num_kv_heads;
+  if (G != 1 && G != 2 && G != 4 && G != 8) return PA_ERR_UNSUPPORTED;
+  const bool f8 = is_8bit(cache->dtype);
+  if ((cache->dtype != PA_BF16 && !f8) || cache->block_size < 8) return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size > INT32_MAX ||
+      max_context_len > kMaxOptionContext)
+    return PA_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * cache->block_size ||
+      max_q_len > max_context_len)
+    return PA_ERR_INVALID_ARG;
+  if (!std::isfinite(scale) || scale <= 0.f) return PA_ERR_INVALID_ARG;
+  if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return PA_OK;
+  if (!q || !cu_q_lens || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(cu_q_lens) & 3) || (reinterpret_cast<uintptr_t>(block_tables) & 3) ||
+      (reinterpret_cast<uintptr_t>(context_lens) & 3))
+    return PA_ERR_INVALID_ARG;
+  const int D = cache->head_dim, tiles_per_cta = D == 128 ? 2 : 1, tt = 128 / G;
+  const int64_t ntiles = ((static_cast<int64_t>(max_q_len) + tt - 1) / tt + tiles_per_cta - 1) / tiles_per_cta;
+  if (num_seqs > 65535 || ntiles > 65535) return PA_ERR_UNSUPPORTED;
+  PrefillArgs a = {};
+  a.q = q;
+  a.cu_q = cu_q_lens;
+  a.tables = block_tables;
+  a.lens = context_lens;
+  a.num_blocks = cache->num_blocks;
+  a.num_seqs = num_seqs;
+  a.hq = num_q_heads;
+  a.hkv = cache->num_kv_heads;
+  a.bs = cache->block_size;
+  a.max_blocks = max_blocks_per_seq;
+  a.max_ctx = max_context_len;
+  a.ntiles = static_cast<int32_t>(ntiles);
+  a.out16 = static_cast<__nv_bfloat16*>(out);
+  a.num_tokens = num_tokens;
+  a.max_q = max_q_len;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float ks = f8 ? cache->k_scale : 1.f;
+  a.scale_log2 = scale * kLog2e * ks;
+  a.v_scale = f8 ? cache->v_scale : 1.f;
+  a.window = max_context_len;
+  if (options) {
+    a.lse = options->lse;
+    a.sinks = options->sinks;
+    if (options->window > 0 && options->window < max_context_len) a.window = options->window;
+    a.cap_log2 = options->softcap * kLog2e;
+    a.cap_arg = options->softcap > 0.f ? 2.f * kLog2e * (scale / options->softcap) * ks : 0.f;
+  }
+  CUtensorMap tk, tv, tq;
+  const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
+  auto enc = f8 ? encode_rows_u8 : encode_rows;
+  if (!enc(&tk, cache->k, rows, D, cache->block_size) || !enc(&tv, cache->v, rows, D, cache->block_size) ||
+      !encode_q_tiles(&tq, const_cast<void*>(q), static_cast<uint64_t>(num_tokens), num_q_heads, D, G))
+    return PA_ERR_CUDA;
+  const dim3 grid(cache->num_kv_heads, num_seqs, static_cast<unsigned>(ntiles));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  auto by_dim = [&](auto cf) -> pa_status {
+    constexpr int CF = decltype(cf)::value;
+    return D == 128 ? launch_prefill_window<128, 2, CF>(a, G, grid, tk, tv, tq, s)
+                    : launch_prefill_window<64, 1, CF>(a, G, grid, tk, tv, tq, s);
+  };
+  if (!f8) return by_dim(std::integral_constant<int, 0>{});
+  return cache->dtype == PA_INT8 ? by_dim(std::integral_constant<int, kCodeS8>{})
+                                 : by_dim(std::integral_constant<int, kCodeE4M3>{});
 }
 
 size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,

@@ -28,6 +28,7 @@
 
 #include "decode_f8.cuh"
 #include "decode_mma.cuh"
+#include "score_rule.cuh"
 
 namespace pa {
 
@@ -53,14 +54,6 @@ struct MultiArgs {
   float v_scale;
 };
 
-// A capped score in base 2, cap_log2 * tanh(y), from z = 2 log2 e * y:
-// tanh(y) = 1 - 2 / (2^z + 1), which is 1 and -1 where 2^z is inf and 0. Its
-// absolute error, a few 2^-24, times a cap of 50 moves a score by 1e-5 at most
-// (the hardware's tanh.approx, at 2^-11, would move it by 2 %).
-__device__ __forceinline__ float capped_score(float z, float cap_log2) {
-  return fmaf(-2.f * cap_log2, __fdividef(1.f, fast_exp2(z) + 1.f), cap_log2);
-}
-
 // The new rows, lengths and key range of a sequence.
 struct MultiSeq {
   int32_t q0, n, L;
@@ -77,7 +70,7 @@ __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bo
     m.n = __ldg(a.cu_q + s + 1) - m.q0;
     if (m.q0 < 0 || m.q0 > a.num_tokens || m.n < 0 || m.n > a.max_q || m.n > a.num_tokens - m.q0) {
       if (report) record_error(PA_ERR_DEVICE_BOUNDS, m.n);
-      m.n = m.q0 < 0 || m.q0 > a.num_tokens || m.n < 0 ? 0 : min(min(m.n, a.max_q), a.num_tokens - m.q0);
+      m.n = 0;
     }
   }
   m.L = __ldg(a.lens + s);
@@ -89,21 +82,6 @@ __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bo
   const int32_t span = m.L - m.first;
   m.nparts = span > a.part_tokens ? (span + a.part_tokens - 1) / a.part_tokens : 1;
   return m;
-}
-
-// The end of a row: (m, l) of all its keys in base 2 with its sink, as the
-// factor of o and the log-sum-exp. A row that sees nothing gives 0 and -inf.
-__device__ __forceinline__ float finish_row(const MultiArgs& a, int h, float m, float l, float& lse) {
-  const float sink = a.sinks ? __ldg(a.sinks + h) * 1.4426950408889634f : -INFINITY;
-  const float M = fmaxf(m, sink);
-  if (M == -INFINITY) {
-    lse = -INFINITY;
-    return 0.f;
-  }
-  const float f = exp2f(m - M);
-  const float den = l * f + exp2f(sink - M);
-  lse = (M + log2f(den)) * 0.6931471805599453f;
-  return f / den * a.v_scale;
 }
 
 template <int D, int NG, int CF>
@@ -512,7 +490,7 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
       continue;
     }
     float lse;
-    const float f = finish_row(a, h, M, l, lse);
+    const float f = finish_row(a.sinks, h, M, l, lse) * a.v_scale;
     const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), y1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
     *reinterpret_cast<uint2*>(a.out + orow * D + d) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
@@ -563,7 +541,7 @@ __global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kern
     }
   }
   float lse;
-  const float f = finish_row(a, ri % a.hq, M, l, lse);
+  const float f = finish_row(a.sinks, ri % a.hq, M, l, lse) * a.v_scale;
   __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * VEC);
 #pragma unroll
   for (int e = 0; e < VEC / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * f, acc[2 * e + 1] * f);

@@ -48,3 +48,13 @@ def test_closed_forms():
     assert not none.any() and l3[0, 0] == -np.inf
     _, l4, _ = options_attention(q[:2], K[:1], V[:1], 1.0, sinks=[0.25])      # the first token is before position 0
     assert l4[0, 0] == 0.25
+
+
+@pytest.mark.parametrize("window,cap,sink", [(0, 0.0, None), (3, 0.0, 0.4), (7, 2.0, None), (1, 1.0, float("-inf"))])
+def test_row_wise_and_matrix_forms_agree(window, cap, sink):
+    from oracle.options import options_attention_masked
+    q, K, V = _qkv(9, 13, 4, 2, seed=3)
+    sinks = None if sink is None else np.full(4, sink)
+    for a, b in zip(options_attention(q, K, V, 0.4, window, cap, sinks),
+                    options_attention_masked(q, K, V, 0.4, window, cap, sinks)):
+        assert np.abs(a - b).max() < 1e-13
