@@ -183,31 +183,57 @@ def pa_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
                                        n, ctypes.byref(c), _stream(k_cache, stream)), "pa_reshape_and_cache")
 
 
-def _token_rows(t: torch.Tensor, name: str, dtype, heads_dim=None) -> int:
+# What the calls below share. They are made once per layer and token, so their
+# checks take the short way while everything is in order.
+
+def _on(t, name, dtype, ndim, device_index):
+    """data_ptr of a contiguous tensor of that dtype and rank on the cache's device."""
+    if t.dtype is not dtype or t.get_device() != device_index or t.dim() != ndim or not t.is_contiguous():
+        _dev(t, name, dtype, ndim)
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device_index}")
+    return t.data_ptr()
+
+
+def _call_on(device_index, fn, what, *args):
+    """fn(*args) with that device current."""
+    if torch.cuda.current_device() == device_index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(device_index):
+            status = fn(*args)
+    if status != PA_OK:
+        raise PagedAttnError(status, what)
+
+
+def _stream_on(device_index, stream) -> int:
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(device_index)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _token_rows(t: torch.Tensor, name: str, dtype, num_tokens, heads, head_dim, device_index) -> int:
     """Elements from one token's [heads][head_dim] row to the next, for a tensor
     whose rows are contiguous (a view of a wider projection's rows, say)."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.dim() != 3 or (heads_dim is not None and tuple(t.shape[1:]) != heads_dim):
-        raise ValueError(f"{name} must be [num_tokens][heads][head_dim], got {tuple(t.shape)}")
-    n, h, d = t.shape
-    if n == 0 or h == 0:
-        return h * d
-    if t.stride(2) != 1 or (h > 1 and t.stride(1) != d):
+    if t.dtype is not dtype or t.get_device() != device_index:
+        if not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device_index}")
+    if t.shape != (num_tokens, heads, head_dim):
+        raise ValueError(f"{name} must be [num_tokens][heads][head_dim] = {(num_tokens, heads, head_dim)}, "
+                         f"got {tuple(t.shape)}")
+    row = heads * head_dim
+    if num_tokens == 0 or row == 0:
+        return row
+    st, sh, sd = t.stride()
+    if sd != 1 or (heads > 1 and sh != head_dim):
         raise ValueError(f"{name}: each token's heads must be contiguous")
-    # torch leaves a single row's stride open: it is never walked
-    stride = t.stride(0) if n > 1 else h * d
-    if stride < h * d:
+    if num_tokens == 1:  # torch leaves a single row's stride open: it is never walked
+        return row
+    if st < row:
         raise ValueError(f"{name}: the tokens' rows overlap")
-    return stride
-
-
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, the cache on {first.device}")
+    return st
 
 
 def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved=False,
@@ -217,29 +243,30 @@ def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     slots and q to q_out. q, k, v: [num_tokens][heads][head_dim], also as views
     of one projection's rows; q and q_out may be None."""
     c = make_cache(k_cache, v_cache)
-    dt, kv = input_dtype(k_cache.dtype), (c.num_kv_heads, c.head_dim)
-    sk, sv = _token_rows(k, "k", dt, kv), _token_rows(v, "v", dt, kv)
+    dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
     n = int(k.shape[0])
+    sk, sv = _token_rows(k, "k", dt, n, hkv, d, dev), _token_rows(v, "v", dt, n, hkv, d, dev)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     sq = hq = 0
+    qp = qo = None
     if q is not None:
-        sq, hq = _token_rows(q, "q", dt), int(q.shape[1])
-        _dev(q_out, "q_out", dt, 3)
-        if tuple(q.shape) != (n, hq, c.head_dim) or q_out.shape != q.shape:
-            raise ValueError("q, q_out must be [num_tokens][num_q_heads][head_dim]")
-    _dev(cos_sin, "cos_sin", torch.float32, 2)
-    if int(v.shape[0]) != n or tuple(positions.shape) != (n,) or tuple(slot_mapping.shape) != (n,):
-        raise ValueError("v, positions and slot_mapping must have a row for every token of k")
-    _same_device(k_cache, v_cache=v_cache, q=q, k=k, v=v, positions=positions, cos_sin=cos_sin,
-                 slot_mapping=slot_mapping, q_out=q_out)
-    with torch.cuda.device(k_cache.device):
-        _check(_lib().pa_rotate_and_cache(q.data_ptr() if q is not None else None, sq, k.data_ptr(), sk, v.data_ptr(),
-                                          sv, _dev(positions, "positions", torch.int32), cos_sin.data_ptr(),
-                                          int(cos_sin.shape[0]), int(cos_sin.shape[1]), 1 if interleaved else 0,
-                                          _dev(slot_mapping, "slot_mapping", torch.int64), n, hq, ctypes.byref(c),
-                                          q_out.data_ptr() if q is not None else None, _stream(k_cache, stream)),
-               "pa_rotate_and_cache")
+        if q.dim() != 3:
+            raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
+        hq = int(q.shape[1])
+        sq, qp, qo = _token_rows(q, "q", dt, n, hq, d, dev), q.data_ptr(), _on(q_out, "q_out", dt, 3, dev)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must be [num_tokens][num_q_heads][head_dim]")
+    table = _on(cos_sin, "cos_sin", torch.float32, 2, dev)
+    pos, slots = _on(positions, "positions", torch.int32, 1, dev), _on(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+    if positions.shape[0] != n or slot_mapping.shape[0] != n:
+        raise ValueError("positions and slot_mapping must have an entry for every token of k")
+    if v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be on one device")
+    max_positions, rotary_dim = cos_sin.shape
+    _call_on(dev, _lib().pa_rotate_and_cache, "pa_rotate_and_cache", qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, pos,
+             table, max_positions, rotary_dim, 1 if interleaved else 0, slots, n, hq, ctypes.byref(c), qo,
+             _stream_on(dev, stream))
 
 
 def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
@@ -360,17 +387,17 @@ def pa_prefill(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale
                              int(max_context_len), float(scale), out.data_ptr(), _stream(q, stream)), "pa_prefill")
 
 
-def _attn_options(window, softcap, sinks, lse, num_tokens, num_q_heads) -> pa_attn_options:
+def _attn_options(window, softcap, sinks, lse, num_tokens, num_q_heads, device_index) -> pa_attn_options:
+    sp = lp = None
     if sinks is not None:
-        _dev(sinks, "sinks", torch.float32, 1)
-        if tuple(sinks.shape) != (num_q_heads,):
+        sp = _on(sinks, "sinks", torch.float32, 1, device_index)
+        if sinks.shape[0] != num_q_heads:
             raise ValueError("sinks must be [num_q_heads]")
     if lse is not None:
-        _dev(lse, "lse", torch.float32, 2)
-        if tuple(lse.shape) != (num_tokens, num_q_heads):
+        lp = _on(lse, "lse", torch.float32, 2, device_index)
+        if lse.shape != (num_tokens, num_q_heads):
             raise ValueError("lse must be [num_tokens][num_q_heads]")
-    return pa_attn_options(int(window), float(softcap), sinks.data_ptr() if sinks is not None else None,
-                           lse.data_ptr() if lse is not None else None)
+    return pa_attn_options(window, softcap, sp, lp)
 
 
 def pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
@@ -379,26 +406,28 @@ def pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads
                                                       head_dim, max_context_len, window, partition_tokens))
 
 
-def _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, **others):
-    """Checks of attention over packed new tokens; (pa_cache, T, Hq, num_seqs)."""
+def _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out):
+    """Checks of attention over packed new tokens. Returns (pa_cache, device
+    index, T, Hq, num_seqs, the pointers of q, cu_q_lens, block_tables,
+    context_lens and out)."""
     c = make_cache(k_cache, v_cache)
-    _dev(q, "q", input_dtype(k_cache.dtype), 3)
-    _dev(out, "out", q.dtype, 3)
+    dev, dt = k_cache.get_device(), input_dtype(k_cache.dtype)
+    qp, op = _on(q, "q", dt, 3, dev), _on(out, "out", dt, 3, dev)
     T, hq, d = q.shape
     if d != c.head_dim or out.shape != q.shape:
         raise ValueError("q/out shape mismatch")
-    _dev(block_tables, "block_tables", torch.int32, 2)
-    _dev(context_lens, "context_lens", torch.int32, 1)
-    n = int(context_lens.shape[0])
+    tp, lp = _on(block_tables, "block_tables", torch.int32, 2, dev), _on(context_lens, "context_lens", torch.int32, 1, dev)
+    n = context_lens.shape[0]
     if block_tables.shape[0] != n:
         raise ValueError("block_tables must have num_seqs rows")
+    cp = None
     if cu_q_lens is not None:
-        _dev(cu_q_lens, "cu_q_lens", torch.int32, 1)
+        cp = _on(cu_q_lens, "cu_q_lens", torch.int32, 1, dev)
         if cu_q_lens.shape[0] != n + 1:
             raise ValueError("cu_q_lens must have num_seqs + 1 entries")
-    _same_device(k_cache, v_cache=v_cache, q=q, out=out, cu_q_lens=cu_q_lens, block_tables=block_tables,
-                 context_lens=context_lens, **others)
-    return c, int(T), int(hq), n
+    if v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be on one device")
+    return c, dev, T, hq, n, qp, cp, tp, lp, op
 
 
 def pa_decode_multi(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale, out, max_q_len, max_context_len,
@@ -406,17 +435,14 @@ def pa_decode_multi(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, 
     """Attention of one or a few new tokens per sequence (rows of q [T][Hq][D] by
     cu_q_lens, or with None one row per sequence) over the paged cache; out has
     q's type, lse (optional) fp32 [T][Hq]. See pagedattn.h."""
-    c, T, hq, n = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, sinks=sinks, lse=lse,
-                               workspace=workspace)
-    opt = _attn_options(window, softcap, sinks, lse, T, hq)
-    ws_ptr, ws_bytes = (None, 0) if workspace is None else (_dev(workspace, "workspace"),
-                                                            workspace.numel() * workspace.element_size())
-    with torch.cuda.device(k_cache.device):
-        _check(_lib().pa_decode_multi(q.data_ptr(), T, n, cu_q_lens.data_ptr() if cu_q_lens is not None else None,
-                                      int(max_q_len), hq, ctypes.byref(c), block_tables.data_ptr(),
-                                      int(block_tables.shape[1]), context_lens.data_ptr(), int(max_context_len),
-                                      float(scale), ctypes.byref(opt), out.data_ptr(), int(partition_tokens), ws_ptr,
-                                      ws_bytes, _stream(k_cache, stream)), "pa_decode_multi")
+    c, dev, T, hq, n, qp, cp, tp, lp, op = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out)
+    opt = _attn_options(window, softcap, sinks, lse, T, hq, dev)
+    ws, ws_bytes = None, 0
+    if workspace is not None:
+        ws, ws_bytes = _on(workspace, "workspace", workspace.dtype, workspace.dim(), dev), workspace.nbytes
+    _call_on(dev, _lib().pa_decode_multi, "pa_decode_multi", qp, T, n, cp, max_q_len, hq, ctypes.byref(c), tp,
+             block_tables.shape[1], lp, max_context_len, scale, ctypes.byref(opt), op, partition_tokens, ws, ws_bytes,
+             _stream_on(dev, stream))
 
 
 def pa_prefill_window(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale, out, max_q_len,
@@ -426,13 +452,10 @@ def pa_prefill_window(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens
     and the log-sum-exp; out has q's type, lse (optional) fp32 [T][Hq]."""
     if cu_q_lens is None:
         raise ValueError("cu_q_lens is needed")
-    c, T, hq, n = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out, sinks=sinks, lse=lse)
-    opt = _attn_options(window, softcap, sinks, lse, T, hq)
-    with torch.cuda.device(k_cache.device):
-        _check(_lib().pa_prefill_window(q.data_ptr(), T, n, cu_q_lens.data_ptr(), int(max_q_len), hq, ctypes.byref(c),
-                                        block_tables.data_ptr(), int(block_tables.shape[1]), context_lens.data_ptr(),
-                                        int(max_context_len), float(scale), ctypes.byref(opt), out.data_ptr(),
-                                        _stream(k_cache, stream)), "pa_prefill_window")
+    c, dev, T, hq, n, qp, cp, tp, lp, op = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out)
+    opt = _attn_options(window, softcap, sinks, lse, T, hq, dev)
+    _call_on(dev, _lib().pa_prefill_window, "pa_prefill_window", qp, T, n, cp, max_q_len, hq, ctypes.byref(c), tp,
+             block_tables.shape[1], lp, max_context_len, scale, ctypes.byref(opt), op, _stream_on(dev, stream))
 
 
 def pa_decode_cascade_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size,

@@ -13,6 +13,7 @@
 #include "decode_f8.cuh"
 #include "decode_mma.cuh"
 #include "decode_multi.cuh"
+#include "decode_multi_tc.cuh"
 #include "decode_simt.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"
@@ -386,27 +387,23 @@ pa_status launch_reduce(const DecodeArgs& a, cudaStream_t st) {
   return launched();
 }
 
-// pa_decode_multi: groups of 8 rows a CTA handles at once.
-int multi_groups(int32_t max_q_len, int32_t G) {
-  const int32_t rows = max_q_len * G;
-  return rows <= 8 ? 1 : (rows <= 16 ? 2 : 4);
-}
+// pa_decode_multi: up to 16 rows (new tokens x query heads of a kv head) on
+// mma.sync, more on tcgen05.
+bool multi_on_tc(int32_t max_q_len, int32_t G) { return max_q_len * G > 16; }
 
 // Its partitions. Returns their size (a multiple of 64, INT32_MAX: no split)
 // and how many the longest sequence has.
 int32_t multi_partition(int32_t num_seqs, int32_t max_q_len, int32_t hq, int32_t hkv, int32_t max_ctx, int32_t window,
-                        int32_t requested, int32_t* parts, int32_t* row_tiles) {
-  const int32_t G = hq / hkv, ng = multi_groups(max_q_len, G);
-  *row_tiles = (max_q_len * G + 8 * ng - 1) / (8 * ng);
+                        int32_t requested, int32_t* parts) {
   int64_t span = max_ctx;
   if (window > 0 && static_cast<int64_t>(window) + max_q_len - 1 < span) span = window + max_q_len - 1;
   span += 63;  // the first key, down to a multiple of 64
   int64_t P = requested;
   if (requested < 0) {
-    const int64_t units = static_cast<int64_t>(num_seqs) * hkv * *row_tiles;
-    const int64_t slots = 148 * (ng == 4 ? 2 : 3);
-    const int64_t want = (2 * slots + units - 1) / units;
-    P = ((span + want - 1) / want + 63) / 64 * 64;
+    const int64_t units = static_cast<int64_t>(num_seqs) * hkv;
+    const int64_t slots = multi_on_tc(max_q_len, hq / hkv) ? 4 * 148 : 6 * 148;
+    const int64_t want = (slots + units - 1) / units;
+    P = ((span + want - 1) / want + 127) / 128 * 128;
     if (P < 256) P = 256;
   }
   if (P <= 0 || P >= span) {
@@ -428,25 +425,23 @@ pa_status check_options(const pa_attn_options* o) {
 
 constexpr int32_t kMaxOptionContext = 1 << 30;  // positions minus windows stay within 32 bits
 
-template <int D, int NG, int CF>
-pa_status launch_multi(const MultiArgs& a, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  using Cfg = MultiCfg<D, NG, CF>;
-  auto kern = decode_multi_kernel<D, NG, CF>;
-  if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, true)) return PA_ERR_CUDA;
-  kern<<<dim3(a.hkv, a.num_seqs, a.max_parts * a.row_tiles), Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, a);
-  const pa_status r = launched();
+template <int D, int CF>
+pa_status launch_multi(const MultiArgs& a, bool on_tc, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
+  const dim3 grid(a.hkv, a.num_seqs, a.max_parts);
+  auto launch = [&](auto kern, int threads, int smem) -> pa_status {
+    if (!smem_attrs(reinterpret_cast<const void*>(kern), smem, true)) return PA_ERR_CUDA;
+    kern<<<grid, threads, smem, st>>>(tk, tv, a);
+    return launched();
+  };
+  using Tc = MultiTcCfg<D, CF>;
+  using C1 = MultiCfg<D, 1, CF>;
+  using C2 = MultiCfg<D, 2, CF>;
+  const pa_status r = on_tc ? launch(decode_multi_tc_kernel<D, CF>, Tc::kThreads, Tc::kSmemBytes)
+                      : (a.max_q << a.gshift) <= 8 ? launch(decode_multi_kernel<D, 1, CF>, C1::kThreads, C1::kSmemBytes)
+                                                   : launch(decode_multi_kernel<D, 2, CF>, C2::kThreads, C2::kSmemBytes);
   if (r != PA_OK || a.max_parts == 1) return r;
   const unsigned rows = static_cast<unsigned>((a.max_q * a.hq + kMultiMergeWarps - 1) / kMultiMergeWarps);
   return launch_kernel(decode_multi_merge_kernel<D>, dim3(rows, a.num_seqs), dim3(32 * kMultiMergeWarps), 0, st, true, a);
-}
-
-template <int D, int CF>
-pa_status dispatch_multi(const MultiArgs& a, int ng, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  switch (ng) {
-    case 1: return launch_multi<D, 1, CF>(a, tk, tv, st);
-    case 2: return launch_multi<D, 2, CF>(a, tk, tv, st);
-    default: return launch_multi<D, 4, CF>(a, tk, tv, st);
-  }
 }
 
 // pa_prefill_window: the prefill kernel with the score rule.
@@ -526,7 +521,7 @@ pa_status pa_rotate_and_cache(const void* q, int64_t q_stride, const void* k, in
   const int32_t hq = q ? num_q_heads : 0;
   const int64_t es = cache->dtype == PA_F32 ? 4 : 2;
   const int64_t heads = static_cast<int64_t>(hq) + 2 * static_cast<int64_t>(hkv);
-  if (heads * (D / 16) > INT32_MAX / 4096) return PA_ERR_UNSUPPORTED;
+  if (heads * D > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if ((q && (q_stride < static_cast<int64_t>(hq) * D || q_stride * es % 16)) ||
       k_stride < static_cast<int64_t>(hkv) * D || k_stride * es % 16 || v_stride < static_cast<int64_t>(hkv) * D ||
       v_stride * es % 16)
@@ -557,18 +552,25 @@ pa_status pa_rotate_and_cache(const void* q, int64_t q_stride, const void* k, in
   a.interleaved = interleaved;
   a.hq = hq;
   a.hkv = hkv;
-  a.bs = cache->block_size;
+  for (a.bshift = 0; (1 << a.bshift) < cache->block_size;) ++a.bshift;
   a.dshift = D == 128 ? 3 : 2;
-  a.units = static_cast<int32_t>(heads * (D / 16));
+  // lanes of D / 16 threads: every head row of a token if they fit, and then as
+  // many tokens as fit
+  const int threads = 256, lanes = threads >> a.dshift;
+  a.lanes = heads < lanes ? static_cast<int32_t>(heads) : lanes;
+  a.tokens = lanes / a.lanes;
+  auto rcp = [](float s) { return s >= 0x1p-100f && s <= 0x1p100f ? 1.f / s : 0.f; };
   a.k_scale = cache->k_scale;
   a.v_scale = cache->v_scale;
-  const int threads = 256;
-  a.tokens_per_cta = a.units >= threads ? 1 : threads / a.units;
-  const unsigned grid = static_cast<unsigned>((static_cast<int64_t>(num_tokens) + a.tokens_per_cta - 1) / a.tokens_per_cta);
-  auto kern = cache->dtype == PA_F32      ? rotate_and_cache_kernel<float, 0>
-              : cache->dtype == PA_BF16   ? rotate_and_cache_kernel<__nv_bfloat16, 0>
-              : cache->dtype == PA_INT8   ? rotate_and_cache_kernel<__nv_bfloat16, kCodeS8>
-                                          : rotate_and_cache_kernel<__nv_bfloat16, kCodeE4M3>;
+  a.k_rcp = rcp(cache->k_scale);
+  a.v_rcp = rcp(cache->v_scale);
+  const int64_t need = (static_cast<int64_t>(num_tokens) + a.tokens - 1) / a.tokens;
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * 4;
+  const unsigned grid = static_cast<unsigned>(need < slots ? need : slots);
+  auto kern = cache->dtype == PA_F32    ? rotate_and_cache_kernel<float, 0>
+              : cache->dtype == PA_BF16 ? rotate_and_cache_kernel<__nv_bfloat16, 0>
+              : cache->dtype == PA_INT8 ? rotate_and_cache_kernel<__nv_bfloat16, kCodeS8>
+                                        : rotate_and_cache_kernel<__nv_bfloat16, kCodeE4M3>;
   kern<<<grid, threads, 0, static_cast<cudaStream_t>(stream)>>>(a);
   return launched();
 }
@@ -869,9 +871,8 @@ size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int
       num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 8 ||
       head_dim <= 0 || max_context_len < 0 || max_context_len > kMaxOptionContext || window < 0 || partition_tokens < -1)
     return 0;
-  int32_t parts, row_tiles;
-  multi_partition(num_seqs, max_q_len, num_q_heads, num_kv_heads, max_context_len, window, partition_tokens, &parts,
-                  &row_tiles);
+  int32_t parts;
+  multi_partition(num_seqs, max_q_len, num_q_heads, num_kv_heads, max_context_len, window, partition_tokens, &parts);
   if (parts == 1) return 0;
   return ml_bytes(num_tokens, num_q_heads, parts) + static_cast<size_t>(num_tokens) * num_q_heads * parts * head_dim * 4;
 }
@@ -906,10 +907,10 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
     return PA_ERR_INVALID_ARG;
   const int32_t window = options ? options->window : 0;
   MultiArgs a;
-  int32_t parts, row_tiles;
+  int32_t parts;
   a.part_tokens = multi_partition(num_seqs, max_q_len, num_q_heads, cache->num_kv_heads, max_context_len, window,
-                                  partition_tokens, &parts, &row_tiles);
-  if (num_seqs > 65535 || static_cast<int64_t>(parts) * row_tiles > 65535) return PA_ERR_UNSUPPORTED;
+                                  partition_tokens, &parts);
+  if (num_seqs > 65535 || parts > 65535) return PA_ERR_UNSUPPORTED;
   const size_t need = pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads,
                                                       cache->num_kv_heads, cache->head_dim, max_context_len, window,
                                                       partition_tokens);
@@ -936,27 +937,28 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
   a.window = window > 0 && window < max_context_len ? window : (max_context_len > 0 ? max_context_len : 1);
   a.max_parts = parts;
-  a.row_tiles = row_tiles;
   constexpr float kLog2e = 1.4426950408889634f;
   const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
   a.scale_log2 = scale * kLog2e * ks;
   a.cap_log2 = cap * kLog2e;
   a.cap_arg = cap > 0.f ? 2.f * kLog2e * (scale / cap) * ks : 0.f;
   a.v_scale = f8 ? cache->v_scale : 1.f;
-  const int D = cache->head_dim, ng = multi_groups(max_q_len, G);
+  const int D = cache->head_dim;
+  const bool on_tc = multi_on_tc(max_q_len, G);
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
   auto enc = [&](CUtensorMap* m, void* base) {
     if (f8) return encode_rows_u8(m, base, rows, D, cache->block_size);
-    return D == 128 ? encode_rows_halves(m, base, rows, cache->block_size) : encode_rows(m, base, rows, D, cache->block_size);
+    return D == 128 && !on_tc ? encode_rows_halves(m, base, rows, cache->block_size)
+                              : encode_rows(m, base, rows, D, cache->block_size);
   };
   if (!enc(&tk, cache->k) || !enc(&tv, cache->v)) return PA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto by_format = [&](auto d) -> pa_status {
     constexpr int DD = decltype(d)::value;
-    if (!f8) return dispatch_multi<DD, 0>(a, ng, tk, tv, s);
-    return cache->dtype == PA_INT8 ? dispatch_multi<DD, kCodeS8>(a, ng, tk, tv, s)
-                                   : dispatch_multi<DD, kCodeE4M3>(a, ng, tk, tv, s);
+    if (!f8) return launch_multi<DD, 0>(a, on_tc, tk, tv, s);
+    return cache->dtype == PA_INT8 ? launch_multi<DD, kCodeS8>(a, on_tc, tk, tv, s)
+                                   : launch_multi<DD, kCodeE4M3>(a, on_tc, tk, tv, s);
   };
   return D == 128 ? by_format(std::integral_constant<int, 128>{}) : by_format(std::integral_constant<int, 64>{});
 }

@@ -11,16 +11,15 @@
 // partitions by M = max m_i, l = sum l_i 2^(m_i - M), o = sum o_i 2^(m_i - M).
 //
 // Bound by HBM: a K/V byte feeds G n multiply-adds (G query heads of a kv head,
-// n new tokens), so up to 32 rows the reads take longer than the products.
-// Rows are (token, head) pairs of one (sequence, kv head): a CTA takes a tile
-// of 8, 16 or 32 of them (NG groups of 8, the MMA's N) and a partition of the
-// visible keys, so every K/V byte is read once per tile. Its products are those
-// of the single-token decode with the tokens as the MMA's M (S^T = K q^T,
-// O^T += V^T P^T), with each K and V fragment used for all NG groups. mma.sync,
-// not tcgen05: its 128-row tile would be three quarters padding or more.
-// The keys a tile sees start at kbeg, inside a 64-key chunk and inside a block:
+// n new tokens), so the reads take longer than the products.
+// Rows are (token, head) pairs of one (sequence, kv head): a CTA takes all of
+// them, up to 16 (NG groups of 8, the MMA's N; more rows: decode_multi_tc.cuh),
+// and a partition of the visible keys, so every K/V byte is read once. Its
+// products are those of the single-token decode with the tokens as the MMA's M
+// (S^T = K q^T, O^T += V^T P^T), with each K and V fragment used for all NG
+// groups. The keys the rows see start at kbeg, inside a 64-key chunk and inside a block:
 // blocks wholly before it are not read, scores outside a row's window are
-// replaced by -inf, V rows outside the tile's keys are zeroed in registers (a
+// replaced by -inf, V rows outside [kbeg, kend) are zeroed in registers (a
 // freed block may hold anything, NaN too).
 // A split sequence's partials are merged by decode_multi_merge_kernel, launched
 // as the programmatic dependent of this grid.
@@ -47,7 +46,7 @@ struct MultiArgs {
   int32_t gshift;          // log2 of hq / hkv
   int32_t window;          // >= 1; max_ctx or more: every earlier key
   int32_t part_tokens;     // a multiple of 64, INT32_MAX: one partition
-  int32_t max_parts, row_tiles;
+  int32_t max_parts;
   float scale_log2;        // scale * log2 e (times the K scale of an 8-bit cache)
   float cap_log2;          // softcap * log2 e, 0: none
   float cap_arg;           // with a cap: 2 log2 e * scale / softcap (times the K scale)
@@ -93,13 +92,11 @@ struct MultiCfg {
   static constexpr int kEl = CF != 0 ? 1 : 2;
   static constexpr int kTileBytes = kChunk * D * kEl;  // K (or V) of one stage
   static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kMinCtas = NG == 4 ? 2 : 3;
+  static constexpr int kMinCtas = 3;
   // the ring of a CTA: its share of the SM's shared memory, and the merge of the warps has to fit
-  static constexpr int kStages = (NG == 4 ? 96 : 64) * 1024 / kStageBytes;
-  static constexpr bool kQSmem = NG == 4;  // q fragments read from shared memory at every step
-  static constexpr int kQBytes = kQSmem ? NG * (D / 16) * 32 * 8 : 0;
+  static constexpr int kStages = 64 * 1024 / kStageBytes;
   static constexpr int kRowPitch = D + 4;  // floats of a row in the merge: lanes' rows in different banks
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + kQBytes;
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes;
   static_assert(kConsumerWarps * kRows * (kRowPitch + 2) * 4 <= kStages * kStageBytes, "merge buffer");
 };
 
@@ -154,20 +151,19 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
 
   const int g = blockIdx.x, s = blockIdx.y;
-  const int p = blockIdx.z / a.row_tiles, tile = blockIdx.z - p * a.row_tiles;
+  const int p = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
-  const MultiSeq ms = load_multi_seq(a, s, g == 0 && blockIdx.z == 0 && tid == 0);
-  const int row0 = tile * Cfg::kRows;
-  const int rows = min(Cfg::kRows, (ms.n << a.gshift) - row0);
+  const MultiSeq ms = load_multi_seq(a, s, g == 0 && p == 0 && tid == 0);
+  const int rows = ms.n << a.gshift;
   if (rows <= 0 || p >= ms.nparts) return;
-  // keys that some row of the tile sees, within the partition
+  // keys that some row sees, within the partition
   const int32_t pos0 = ms.L - ms.n;  // position of the sequence's first new token
-  const int32_t pos_lo = pos0 + (row0 >> a.gshift), pos_hi = pos0 + ((row0 + rows - 1) >> a.gshift);
+  const int32_t pos_lo = pos0, pos_hi = pos0 + ms.n - 1;
   const int32_t t0 = ms.nparts > 1 ? ms.first + p * a.part_tokens : 0;
   const int32_t t1 = ms.nparts > 1 && p < ms.nparts - 1 ? t0 + a.part_tokens : ms.L;
   const int32_t kbeg = max(t0, max(0, pos_lo - a.window + 1));
-  const int32_t kend = min(t1, pos_hi + 1);
+  const int32_t kend = t1;
   const int32_t c_begin = kbeg & ~(C - 1);
   const int nchunks = kend > kbeg ? (kend - c_begin + C - 1) / C : 0;
 
@@ -180,13 +176,12 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
     prefetch_tmap(&tmv);
     pipe_init<S>(ps, NW);
   }
-  // q as the B fragments of S^T (column r of group gi = row 8 gi + r of the
-  // tile, zeros past its rows): dims (2c, 2c + 1) and (+8) of a 16-dim step, or
+  // q as the B fragments of S^T (column r of group gi = row 8 gi + r, zeros
+  // past the last): dims (2c, 2c + 1) and (+8) of a 16-dim step, or
   // over an 8-bit cache, as f16, dims (4c, 4c + 1) and (4c + 2, 4c + 3)
   auto q_frag = [&](int gi, int kk) -> uint2 {
-    const int row = 8 * gi + r;
-    if (row >= rows) return make_uint2(0u, 0u);
-    const int rho = row0 + row;
+    const int rho = 8 * gi + r;
+    if (rho >= rows) return make_uint2(0u, 0u);
     const int64_t qrow = static_cast<int64_t>(ms.q0 + (rho >> a.gshift)) * a.hq + (g << a.gshift) +
                          (rho & ((1 << a.gshift) - 1));
     const uint32_t* w = reinterpret_cast<const uint32_t*>(a.q + qrow * D) + kk * 8;
@@ -197,17 +192,12 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
       return make_uint2(__ldg(w + c), __ldg(w + 4 + c));
     }
   };
-  uint2* qs = reinterpret_cast<uint2*>(sgen + S * Cfg::kStageBytes);
-  uint2 qr[Cfg::kQSmem ? 1 : NG][Cfg::kQSmem ? 1 : KS];
+  uint2 qr[NG][KS];
   if (warp < NW) {
-    if constexpr (Cfg::kQSmem) {
-      for (int i = warp; i < NG * KS; i += NW) qs[i * 32 + lane] = q_frag(i / KS, i % KS);
-    } else {
 #pragma unroll
-      for (int gi = 0; gi < NG; ++gi)
+    for (int gi = 0; gi < NG; ++gi)
 #pragma unroll
-        for (int kk = 0; kk < KS; ++kk) qr[gi][kk] = q_frag(gi, kk);
-    }
+      for (int kk = 0; kk < KS; ++kk) qr[gi][kk] = q_frag(gi, kk);
   }
   __syncthreads();
 
@@ -221,9 +211,9 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
   }
 
   if (warp == NW) {
-    // ---- producer: the blocks of chunk i that hold a key of the tile ----
+    // ---- producer: the blocks of chunk i that hold a key in [kbeg, kend) ----
     const uint32_t box_bytes = static_cast<uint32_t>(a.bs) * D * Cfg::kEl;
-    const uint64_t pol = a.row_tiles > 1 ? l2_evict_normal_policy() : kv_stream_policy();
+    const uint64_t pol = kv_stream_policy();
     pipe_produce<S>(ps, nchunks, [&](int i, int st) {
       const int32_t c0 = c_begin + i * C;
       const int32_t nb = (min(C, kend - c0) + a.bs - 1) / a.bs;  // <= 8 (bs >= 8)
@@ -257,7 +247,7 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = 8 * gi + 2 * c + j;
-        pos[gi][j] = row < rows ? pos0 + ((row0 + row) >> a.gshift) : -1;
+        pos[gi][j] = row < rows ? pos0 + (row >> a.gshift) : -1;
       }
     const int mk = lane >> 3, ik = lane & 7;
     for (int i = 0; i < nchunks; ++i) {
@@ -282,7 +272,7 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
             ldsm_x4(kbase + (d0 >> 6) * hstride + ((((d0 & 63) >> 3) ^ (tokK & 7)) << 4), m0, m1, m2, m3);
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-              const uint2 qq = Cfg::kQSmem ? qs[(gi * KS + kk) * 32 + lane] : qr[Cfg::kQSmem ? 0 : gi][Cfg::kQSmem ? 0 : kk];
+              const uint2 qq = qr[gi][kk];
               if constexpr (NG == 1)
                 mma16x8(kk & 1 ? s1 : x[gi], m0, m2, m1, m3, qq.x, qq.y);  // two chains
               else
@@ -313,7 +303,7 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
             widen4<CF>(w1, k10, k11);
 #pragma unroll
             for (int gi = 0; gi < NG; ++gi) {
-              const uint2 qq = Cfg::kQSmem ? qs[(gi * KS + kk) * 32 + lane] : qr[Cfg::kQSmem ? 0 : gi][Cfg::kQSmem ? 0 : kk];
+              const uint2 qq = qr[gi][kk];
               if constexpr (NG == 1)
                 mma16x8_f16(kk & 1 ? s1 : x[gi], k00, k10, k01, k11, qq.x, qq.y);
               else
@@ -324,8 +314,8 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[0][e] += s1[e];
         }
-        // base-2 scores; -inf outside a row's keys (every row of the tile sees
-        // all 16 keys in most chunks). A key past kend is past its row's position
+        // base-2 scores; -inf outside a row's keys (every row sees all 16 keys
+        // in most chunks). A key past kend is past its row's position
         // or in the next partition, one before kbeg before every window.
         if (a.cap_log2 > 0.f) {
 #pragma unroll
@@ -480,9 +470,8 @@ __global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG,
         acc.w = fmaf(v.w, f, acc.w);
       }
     }
-    const int rho = row0 + row;
-    const int h = (g << a.gshift) + (rho & ((1 << a.gshift) - 1));
-    const int64_t orow = static_cast<int64_t>(ms.q0 + (rho >> a.gshift)) * a.hq + h;
+    const int h = (g << a.gshift) + (row & ((1 << a.gshift) - 1));
+    const int64_t orow = static_cast<int64_t>(ms.q0 + (row >> a.gshift)) * a.hq + h;
     if (ms.nparts > 1) {
       const int64_t prow = orow * a.max_parts + p;
       *reinterpret_cast<float4*>(a.ws_o + prow * D + d) = acc;

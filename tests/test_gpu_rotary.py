@@ -160,6 +160,36 @@ def test_offsets_past_32_bits():
     assert int((vc.view(torch.int16)[-16:] != 0).any(-1).sum()) == 2 * hkv
 
 
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("k_scale,v_scale", [(0.1, 3e-33), (2.0 ** -6, 7.3), (1.7e36, 1e-3)])
+def test_codes_at_any_scale(dtype, k_scale, v_scale):
+    """Codes bit for bit at scales whose reciprocal is exact, rounded and out of
+    the usual range, for values next to and on the borders between codes."""
+    g = torch.Generator().manual_seed(2)
+    n, hkv, D = 64, 2, 128
+    k, v = (torch.randn(n, hkv, D, generator=g) * s * 40 for s in (k_scale, v_scale))
+    # half of the values on multiples of half a code's step
+    k[::2], v[::2] = ((x[::2] / s * 2).round() / 2 * s for x, s in ((k, k_scale), (v, v_scale)))
+    k, v = k.bfloat16(), v.bfloat16()
+    k[1, 0, :4] = torch.tensor([float("inf"), -float("inf"), 0.0, -0.0])
+    v[1, 0, :4] = torch.tensor([3e38, -3e38, 1e-40, float("inf")])
+    kc = torch.zeros(8, hkv, 8, D, dtype=DT[dtype], device="cuda")
+    vc = torch.zeros_like(kc)
+    B.set_kv_scales(kc, vc, k_scale, v_scale)
+    slots, pos = torch.arange(n), torch.zeros(n, dtype=torch.int32)   # position 0: k as it is
+    B.pa_rotate_and_cache(None, k.cuda(), v.cuda(), pos.cuda(), B.rotary_table(1, D), slots.cuda(), kc, vc, None)
+    for pool, x, scale in ((kc, k, k_scale), (vc, v, v_scale)):
+        x32 = x.float().numpy()
+        if pool is kc:   # a 1 - b 0 and b 1 + a 0: an infinity's partner is NaN
+            with np.errstate(invalid="ignore"):
+                x32 = rotate(x32, np.ones((n, D // 2), np.float32), np.zeros((n, D // 2), np.float32), False)
+        got = _bits(pool.cpu()).transpose(1, 2).reshape(n, hkv, D)
+        want = _as_stored(np.ascontiguousarray(x32), dtype, scale).view(torch.uint8)
+        nan = torch.from_numpy(np.isnan(x32))
+        assert torch.equal(got[~nan], want[~nan])
+        assert ((got[nan] & 0x7F) == (0x7F if dtype == "e4m3" else 0)).all()
+
+
 def test_wrong_tensors_are_refused():
     qkv, (q, k, v), slots, pos, kc, vc = _case(8, 6, 4, 2, 64, 8, "bf16", 64)
     table = B.rotary_table(100, 64)

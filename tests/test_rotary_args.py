@@ -41,21 +41,18 @@ def test_cache_checks_and_empty_call():
 
 
 def test_token_rows_of_views():
+    """(On the host, whose device index is -1.)"""
     dt = torch.bfloat16
     fused = torch.zeros(5, 12 * 64, dtype=dt)
-
-    def rows(t):
-        with pytest.MonkeyPatch.context() as m:
-            m.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
-            return B._token_rows(t, "k", dt, (2, 64))
+    rows = lambda t, n=5: B._token_rows(t, "k", dt, n, 2, 64, -1)
     assert rows(fused[:, 128:256].unflatten(1, (2, 64))) == 768
-    assert rows(fused[:, 128:256].unflatten(1, (2, 64))[:1]) == 128
-    assert rows(torch.zeros(0, 2, 64, dtype=dt)) == 128
+    assert rows(fused[:, 128:256].unflatten(1, (2, 64))[:1], 1) == 128
+    assert rows(torch.zeros(0, 2, 64, dtype=dt), 0) == 128
     for bad in (fused[:, :256:2].unflatten(1, (2, 64)), torch.zeros(5, 64, 2, dtype=dt).transpose(1, 2),
-                torch.zeros(1, 2, 64, dtype=dt).expand(5, 2, 64), torch.zeros(5, 3, 64, dtype=dt)):
+                torch.zeros(1, 2, 64, dtype=dt).expand(5, 2, 64), torch.zeros(5, 3, 64, dtype=dt),
+                torch.zeros(4, 2, 64, dtype=dt), torch.zeros(5, 128, dtype=dt)):
         with pytest.raises(ValueError):
             rows(bad)
-    with pytest.raises(TypeError):
-        B._token_rows(fused.unflatten(1, (12, 64)), "k", dt)   # on the host
-    with pytest.raises(TypeError):
-        rows(torch.zeros(5, 2, 64))
+    for device_index, t in ((0, fused.unflatten(1, (12, 64))), (0, torch.zeros(5, 2, 64))):
+        with pytest.raises(TypeError):
+            B._token_rows(t, "k", dt, 5, 2, 64, device_index)
