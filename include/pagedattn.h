@@ -383,8 +383,9 @@ typedef struct {
 
 /*
  * Decode attention of one or a few new tokens per sequence (a decode step, or
- * drafted tokens that are checked in one pass; batches may mix both), split
- * over the cache's length where that fills the GPU. Every new token attends,
+ * drafted tokens that are checked in one pass; batches may mix both). The keys of
+ * the whole batch are divided evenly among the GPU's SMs, sequences split where a
+ * share ends, and the parts joined by a log-sum-exp merge. Every new token attends,
  * through the block table, to the keys of its window up to and including its
  * own (already appended), by the rule of `options`.
  *
@@ -407,9 +408,9 @@ typedef struct {
  *                  every window are not used (those blocks may have been freed).
  *   scale          > 0.
  *   out            device bf16 [num_tokens][num_q_heads][head_dim].
- *   partition_tokens  -1: chosen by the library; 0: no split; else a multiple of
- *                  64: each sequence's keys, from the 64-key boundary at or before
- *                  the first one seen, in partitions of that many.
+ *   partition_tokens  -1: even shares, as above; 0: no split, a (sequence, kv head)
+ *                  each; > 0, a multiple of 64: shares of that many keys (rounded
+ *                  up to the kernel's chunks of 64 or 128).
  *   workspace      >= pa_decode_multi_workspace_bytes(...) bytes, 256-byte aligned;
  *                  may be NULL where that is 0. Its contents need no initial value.
  * q, out and workspace 16-byte aligned. Accumulation is fp32; the result is
@@ -426,8 +427,8 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
                           float scale, const pa_attn_options* options, void* out, int32_t partition_tokens,
                           void* workspace, size_t workspace_bytes, pa_stream stream);
 
-/* Workspace bytes of pa_decode_multi for these sizes (0 where it does not
- * split). window as in pa_attn_options; partition_tokens may be -1. */
+/* Workspace bytes of pa_decode_multi for these sizes, over a cache of any dtype
+ * (0 where it cannot split). window as in pa_attn_options. */
 size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                                        int32_t window, int32_t partition_tokens);

@@ -387,31 +387,43 @@ pa_status launch_reduce(const DecodeArgs& a, cudaStream_t st) {
   return launched();
 }
 
-// pa_decode_multi: up to 16 rows (new tokens x query heads of a kv head) on
+// pa_decode_multi: up to 8 rows (new tokens x query heads of a kv head) on
 // mma.sync, more on tcgen05.
-bool multi_on_tc(int32_t max_q_len, int32_t G) { return max_q_len * G > 16; }
+struct MultiPlan {
+  bool on_tc;
+  int32_t rows;     // of a unit, at most
+  int32_t per;      // MultiArgs::per
+  int64_t workers;  // CTAs
+  bool split;       // workers may share units
+  size_t ws_bytes;  // 2 partials a worker: (m, l) of their rows, 256-aligned, then o
+};
 
-// Its partitions. Returns their size (a multiple of 64, INT32_MAX: no split)
-// and how many the longest sequence has.
-int32_t multi_partition(int32_t num_seqs, int32_t max_q_len, int32_t hq, int32_t hkv, int32_t max_ctx, int32_t window,
-                        int32_t requested, int32_t* parts) {
-  int64_t span = max_ctx;
+size_t multi_ml_bytes(const MultiPlan& p) { return (static_cast<size_t>(2 * p.workers) * p.rows * 8 + 255) / 256 * 256; }
+
+MultiPlan multi_plan(int32_t num_seqs, int32_t max_q_len, int32_t G, int32_t hkv, int32_t D, bool f8, int32_t max_ctx,
+                     int32_t window, int32_t partition_tokens) {
+  MultiPlan p;
+  p.rows = max_q_len * G;
+  p.on_tc = p.rows > 8;
+  const int64_t chunk = p.on_tc ? 128 : (f8 ? 128 : 64);
+  int64_t span = max_ctx;  // keys of a unit, from a multiple of 64 on
   if (window > 0 && static_cast<int64_t>(window) + max_q_len - 1 < span) span = window + max_q_len - 1;
-  span += 63;  // the first key, down to a multiple of 64
-  int64_t P = requested;
-  if (requested < 0) {
-    const int64_t units = static_cast<int64_t>(num_seqs) * hkv;
-    const int64_t slots = multi_on_tc(max_q_len, hq / hkv) ? 4 * 148 : 6 * 148;
-    const int64_t want = (slots + units - 1) / units;
-    P = ((span + want - 1) / want + 127) / 128 * 128;
-    if (P < 256) P = 256;
+  span += 63;
+  const int64_t units = static_cast<int64_t>(num_seqs) * hkv, most = (span + chunk - 1) / chunk;
+  if (partition_tokens == 0) {
+    p.per = kWholeUnits;
+    p.workers = units;
+  } else if (partition_tokens > 0) {
+    p.per = static_cast<int32_t>((partition_tokens + chunk - 1) / chunk);
+    p.workers = (units * most + p.per - 1) / p.per;
+  } else {
+    p.per = 0;
+    p.workers = static_cast<int64_t>(device_sm_count()) * (p.on_tc ? 1 : 3);
+    if (p.workers > units * most) p.workers = units * most;
   }
-  if (P <= 0 || P >= span) {
-    *parts = 1;
-    return INT32_MAX;
-  }
-  *parts = static_cast<int32_t>((span + P - 1) / P);
-  return static_cast<int32_t>(P);
+  p.split = partition_tokens != 0 && most > 1 && p.workers > 1;
+  p.ws_bytes = p.split ? multi_ml_bytes(p) + static_cast<size_t>(2 * p.workers) * p.rows * D * 4 : 0;
+  return p;
 }
 
 // The options of pa_decode_multi and pa_prefill_window.
@@ -426,33 +438,38 @@ pa_status check_options(const pa_attn_options* o) {
 constexpr int32_t kMaxOptionContext = 1 << 30;  // positions minus windows stay within 32 bits
 
 template <int D, int CF>
-pa_status launch_multi(const MultiArgs& a, bool on_tc, const CUtensorMap& tk, const CUtensorMap& tv, cudaStream_t st) {
-  const dim3 grid(a.hkv, a.num_seqs, a.max_parts);
+pa_status launch_multi(const MultiArgs& a, const MultiPlan& p, const CUtensorMap& tk, const CUtensorMap& tv,
+                       cudaStream_t st) {
+  using Tc = MultiTcCfg<D, CF>;
+  using Mma = MultiCfg<D, CF>;
   auto launch = [&](auto kern, int threads, int smem) -> pa_status {
     if (!smem_attrs(reinterpret_cast<const void*>(kern), smem, true)) return PA_ERR_CUDA;
-    kern<<<grid, threads, smem, st>>>(tk, tv, a);
+    kern<<<static_cast<unsigned>(p.workers), threads, smem, st>>>(tk, tv, a);
     return launched();
   };
-  using Tc = MultiTcCfg<D, CF>;
-  using C1 = MultiCfg<D, 1, CF>;
-  using C2 = MultiCfg<D, 2, CF>;
-  const pa_status r = on_tc ? launch(decode_multi_tc_kernel<D, CF>, Tc::kThreads, Tc::kSmemBytes)
-                      : (a.max_q << a.gshift) <= 8 ? launch(decode_multi_kernel<D, 1, CF>, C1::kThreads, C1::kSmemBytes)
-                                                   : launch(decode_multi_kernel<D, 2, CF>, C2::kThreads, C2::kSmemBytes);
-  if (r != PA_OK || a.max_parts == 1) return r;
-  const unsigned rows = static_cast<unsigned>((a.max_q * a.hq + kMultiMergeWarps - 1) / kMultiMergeWarps);
-  return launch_kernel(decode_multi_merge_kernel<D>, dim3(rows, a.num_seqs), dim3(32 * kMultiMergeWarps), 0, st, true, a);
+  pa_status r;
+  if (!p.on_tc)
+    r = launch(decode_multi_kernel<D, CF>, Mma::kThreads, Mma::kSmemBytes);
+  else if (p.rows <= 32)
+    r = launch(decode_multi_tc_kernel<D, CF, 4>, Tc::kThreads, Tc::kSmemBytes);
+  else if (p.rows <= 64)
+    r = launch(decode_multi_tc_kernel<D, CF, 2>, Tc::kThreads, Tc::kSmemBytes);
+  else
+    r = launch(decode_multi_tc_kernel<D, CF, 1>, Tc::kThreads, Tc::kSmemBytes);
+  if (r != PA_OK || !p.split) return r;
+  auto merge = p.on_tc ? decode_multi_merge_kernel<D, Tc::kKeys, Tc::kMinChunks>
+                       : decode_multi_merge_kernel<D, Mma::kChunk, Mma::kMinChunks>;
+  const dim3 grid(static_cast<unsigned>(p.workers - 1), (p.rows + kMultiMergeWarps - 1) / kMultiMergeWarps);
+  return launch_kernel(merge, grid, dim3(32 * kMultiMergeWarps), 0, st, true, a);
 }
 
 // pa_prefill_window: the prefill kernel with the score rule.
-template <int D, int TILES, int CF>
-pa_status launch_prefill_window(const PrefillArgs& a, int G, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
+template <int D, int CF>
+pa_status launch_prefill_window(const PrefillArgs& a, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tq, cudaStream_t st) {
+  constexpr int TILES = 2;
   using Cfg = TcCfg<D, TILES, CF != 0>;
-  auto kern = G == 1   ? prefill_tc_kernel<D, 1, TILES, CF, true>
-              : G == 2 ? prefill_tc_kernel<D, 2, TILES, CF, true>
-              : G == 4 ? prefill_tc_kernel<D, 4, TILES, CF, true>
-                       : prefill_tc_kernel<D, 8, TILES, CF, true>;
+  auto kern = prefill_tc_kernel<D, 0, TILES, CF, true>;
   if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, false)) return PA_ERR_CUDA;
   kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, tq, tq, a);  // (no output map: O goes out through plain stores)
   return launched();
@@ -815,8 +832,8 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
       (reinterpret_cast<uintptr_t>(cu_q_lens) & 3) || (reinterpret_cast<uintptr_t>(block_tables) & 3) ||
       (reinterpret_cast<uintptr_t>(context_lens) & 3))
     return PA_ERR_INVALID_ARG;
-  const int D = cache->head_dim, tiles_per_cta = D == 128 ? 2 : 1, tt = 128 / G;
-  const int64_t ntiles = ((static_cast<int64_t>(max_q_len) + tt - 1) / tt + tiles_per_cta - 1) / tiles_per_cta;
+  const int D = cache->head_dim, tt = 2 * (128 / G);  // tokens of a CTA: two query tiles
+  const int64_t ntiles = (static_cast<int64_t>(max_q_len) + tt - 1) / tt;
   if (num_seqs > 65535 || ntiles > 65535) return PA_ERR_UNSUPPORTED;
   PrefillArgs a = {};
   a.q = q;
@@ -834,6 +851,7 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
   a.out16 = static_cast<__nv_bfloat16*>(out);
   a.num_tokens = num_tokens;
   a.max_q = max_q_len;
+  a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
   constexpr float kLog2e = 1.4426950408889634f;
   const float ks = f8 ? cache->k_scale : 1.f;
   a.scale_log2 = scale * kLog2e * ks;
@@ -844,7 +862,8 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
     a.sinks = options->sinks;
     if (options->window > 0 && options->window < max_context_len) a.window = options->window;
     a.cap_log2 = options->softcap * kLog2e;
-    a.cap_arg = options->softcap > 0.f ? 2.f * kLog2e * (scale / options->softcap) * ks : 0.f;
+    a.cap_k = options->softcap > 0.f ? scale / options->softcap * ks : 0.f;
+    a.cap_arg = 2.f * kLog2e * a.cap_k;
   }
   CUtensorMap tk, tv, tq;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
@@ -856,8 +875,8 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto by_dim = [&](auto cf) -> pa_status {
     constexpr int CF = decltype(cf)::value;
-    return D == 128 ? launch_prefill_window<128, 2, CF>(a, G, grid, tk, tv, tq, s)
-                    : launch_prefill_window<64, 1, CF>(a, G, grid, tk, tv, tq, s);
+    return D == 128 ? launch_prefill_window<128, CF>(a, grid, tk, tv, tq, s)
+                    : launch_prefill_window<64, CF>(a, grid, tk, tv, tq, s);
   };
   if (!f8) return by_dim(std::integral_constant<int, 0>{});
   return cache->dtype == PA_INT8 ? by_dim(std::integral_constant<int, kCodeS8>{})
@@ -871,10 +890,13 @@ size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int
       num_q_heads <= 0 || num_kv_heads <= 0 || num_q_heads % num_kv_heads || num_q_heads / num_kv_heads > 8 ||
       head_dim <= 0 || max_context_len < 0 || max_context_len > kMaxOptionContext || window < 0 || partition_tokens < -1)
     return 0;
-  int32_t parts;
-  multi_partition(num_seqs, max_q_len, num_q_heads, num_kv_heads, max_context_len, window, partition_tokens, &parts);
-  if (parts == 1) return 0;
-  return ml_bytes(num_tokens, num_q_heads, parts) + static_cast<size_t>(num_tokens) * num_q_heads * parts * head_dim * 4;
+  size_t need = 0;  // for a cache of either element size
+  for (const bool f8 : {false, true}) {
+    const size_t n = multi_plan(num_seqs, max_q_len, num_q_heads / num_kv_heads, num_kv_heads, head_dim, f8,
+                                max_context_len, window, partition_tokens).ws_bytes;
+    if (n > need) need = n;
+  }
+  return need;
 }
 
 pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
@@ -906,16 +928,12 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
       (reinterpret_cast<uintptr_t>(context_lens) & 3))
     return PA_ERR_INVALID_ARG;
   const int32_t window = options ? options->window : 0;
-  MultiArgs a;
-  int32_t parts;
-  a.part_tokens = multi_partition(num_seqs, max_q_len, num_q_heads, cache->num_kv_heads, max_context_len, window,
-                                  partition_tokens, &parts);
-  if (num_seqs > 65535 || parts > 65535) return PA_ERR_UNSUPPORTED;
-  const size_t need = pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads,
-                                                      cache->num_kv_heads, cache->head_dim, max_context_len, window,
-                                                      partition_tokens);
-  if (need && (!workspace || workspace_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
+  const MultiPlan plan = multi_plan(num_seqs, max_q_len, G, cache->num_kv_heads, cache->head_dim, f8, max_context_len,
+                                    window, partition_tokens);
+  if (plan.workers > INT32_MAX) return PA_ERR_UNSUPPORTED;
+  if (plan.split && (!workspace || workspace_bytes < plan.ws_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return PA_ERR_INVALID_ARG;
+  MultiArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.cu_q = cu_q_lens;
   a.tables = block_tables;
@@ -924,7 +942,7 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.out = static_cast<__nv_bfloat16*>(out);
   a.lse = options ? options->lse : nullptr;
   a.ws_ml = static_cast<float*>(workspace);
-  a.ws_o = reinterpret_cast<float*>(static_cast<char*>(workspace) + ml_bytes(num_tokens, num_q_heads, parts));
+  a.ws_o = plan.split ? reinterpret_cast<float*>(static_cast<char*>(workspace) + multi_ml_bytes(plan)) : nullptr;
   a.num_blocks = cache->num_blocks;
   a.num_seqs = num_seqs;
   a.num_tokens = num_tokens;
@@ -936,29 +954,30 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.max_ctx = max_context_len;
   a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
   a.window = window > 0 && window < max_context_len ? window : (max_context_len > 0 ? max_context_len : 1);
-  a.max_parts = parts;
+  a.per = plan.per;
+  a.slot_rows = plan.rows;
   constexpr float kLog2e = 1.4426950408889634f;
   const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
   a.scale_log2 = scale * kLog2e * ks;
   a.cap_log2 = cap * kLog2e;
-  a.cap_arg = cap > 0.f ? 2.f * kLog2e * (scale / cap) * ks : 0.f;
+  a.cap_k = cap > 0.f ? scale / cap * ks : 0.f;
+  a.cap_arg = 2.f * kLog2e * a.cap_k;
   a.v_scale = f8 ? cache->v_scale : 1.f;
   const int D = cache->head_dim;
-  const bool on_tc = multi_on_tc(max_q_len, G);
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
   auto enc = [&](CUtensorMap* m, void* base) {
     if (f8) return encode_rows_u8(m, base, rows, D, cache->block_size);
-    return D == 128 && !on_tc ? encode_rows_halves(m, base, rows, cache->block_size)
+    return D == 128 && !plan.on_tc ? encode_rows_halves(m, base, rows, cache->block_size)
                               : encode_rows(m, base, rows, D, cache->block_size);
   };
   if (!enc(&tk, cache->k) || !enc(&tv, cache->v)) return PA_ERR_CUDA;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto by_format = [&](auto d) -> pa_status {
     constexpr int DD = decltype(d)::value;
-    if (!f8) return launch_multi<DD, 0>(a, on_tc, tk, tv, s);
-    return cache->dtype == PA_INT8 ? launch_multi<DD, kCodeS8>(a, on_tc, tk, tv, s)
-                                   : launch_multi<DD, kCodeE4M3>(a, on_tc, tk, tv, s);
+    if (!f8) return launch_multi<DD, 0>(a, plan, tk, tv, s);
+    return cache->dtype == PA_INT8 ? launch_multi<DD, kCodeS8>(a, plan, tk, tv, s)
+                                   : launch_multi<DD, kCodeE4M3>(a, plan, tk, tv, s);
   };
   return D == 128 ? by_format(std::integral_constant<int, 128>{}) : by_format(std::integral_constant<int, 64>{});
 }

@@ -11,18 +11,17 @@
 // partitions by M = max m_i, l = sum l_i 2^(m_i - M), o = sum o_i 2^(m_i - M).
 //
 // Bound by HBM: a K/V byte feeds G n multiply-adds (G query heads of a kv head,
-// n new tokens), so the reads take longer than the products.
-// Rows are (token, head) pairs of one (sequence, kv head): a CTA takes all of
-// them, up to 16 (NG groups of 8, the MMA's N; more rows: decode_multi_tc.cuh),
-// and a partition of the visible keys, so every K/V byte is read once. Its
-// products are those of the single-token decode with the tokens as the MMA's M
-// (S^T = K q^T, O^T += V^T P^T), with each K and V fragment used for all NG
-// groups. The keys the rows see start at kbeg, inside a 64-key chunk and inside a block:
-// blocks wholly before it are not read, scores outside a row's window are
-// replaced by -inf, V rows outside [kbeg, kend) are zeroed in registers (a
-// freed block may hold anything, NaN too).
-// A split sequence's partials are merged by decode_multi_merge_kernel, launched
-// as the programmatic dependent of this grid.
+// n new tokens), so the reads take longer than the products. The rows, (token,
+// head) pairs of one (sequence, kv head), are handled together, so every K/V byte
+// is read once; what is left is to keep the reads going to the end on every SM,
+// whatever the lengths: see MultiWork. This kernel takes up to 8 rows, the N of
+// its MMAs (more: decode_multi_tc.cuh); its products are those of the single-token
+// decode with the tokens as the MMA's M (S^T = K q^T, O^T += V^T P^T), over an
+// 8-bit cache two 16-key tiles of a warp at a time (twice the conversions per
+// byte: two independent chains hide each other's latency). The keys the rows see
+// start inside a chunk and inside a block: blocks wholly before them are not
+// read, scores outside a row's window are replaced by -inf, V rows outside [kbeg,
+// kend) are zeroed in registers (a freed block may hold anything, NaN too).
 #pragma once
 
 #include "decode_f8.cuh"
@@ -39,25 +38,28 @@ struct MultiArgs {
   const float* sinks;      // [hq] or null
   __nv_bfloat16* out;      // [num_tokens][hq][D]
   float* lse;              // [num_tokens][hq] or null
-  float* ws_ml;            // [num_tokens][hq][max_parts][2]
-  float* ws_o;             // [num_tokens][hq][max_parts][D]
+  float* ws_ml;            // [2 workers][slot_rows][2]
+  float* ws_o;             // [2 workers][slot_rows][D]
   int64_t num_blocks;
   int32_t num_seqs, num_tokens, max_q, hq, hkv, bs, max_blocks, max_ctx;
   int32_t gshift;          // log2 of hq / hkv
   int32_t window;          // >= 1; max_ctx or more: every earlier key
-  int32_t part_tokens;     // a multiple of 64, INT32_MAX: one partition
-  int32_t max_parts;
+  int32_t per;             // chunks of a worker; 0: even shares, kWholeUnits: a unit each
+  int32_t slot_rows;       // rows of a partial: max_q hq / hkv
   float scale_log2;        // scale * log2 e (times the K scale of an 8-bit cache)
   float cap_log2;          // softcap * log2 e, 0: none
-  float cap_arg;           // with a cap: 2 log2 e * scale / softcap (times the K scale)
+  float cap_k;             // with a cap: scale / softcap (times the K scale)
+  float cap_arg;           // 2 log2 e * cap_k
   float v_scale;
 };
 
-// The new rows, lengths and key range of a sequence.
+// The new rows and length of a sequence, and the start of its chunks.
 struct MultiSeq {
   int32_t q0, n, L;
-  int32_t first;   // 64-aligned start of the sequence's partitions
-  int32_t nparts;
+  int32_t first;  // the first key any of its rows sees, down to a multiple of 64
+  __device__ __forceinline__ int32_t chunks(int keys) const {
+    return n <= 0 ? 0 : max(1, (L - first + keys - 1) / keys);
+  }
 };
 
 __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bool report) {
@@ -78,462 +80,553 @@ __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bo
     m.L = m.L < 0 ? 0 : min(m.L, a.max_ctx);
   }
   m.first = max(0, m.L - m.n - a.window + 1) & ~63;
-  const int32_t span = m.L - m.first;
-  m.nparts = span > a.part_tokens ? (span + a.part_tokens - 1) / a.part_tokens : 1;
   return m;
 }
 
-template <int D, int NG, int CF>
-struct MultiCfg {
-  static constexpr int kConsumerWarps = 4;
-  static constexpr int kThreads = 32 * (kConsumerWarps + 1);
-  static constexpr int kChunk = 64;
-  static constexpr int kRows = 8 * NG;
-  static constexpr int kEl = CF != 0 ? 1 : 2;
-  static constexpr int kTileBytes = kChunk * D * kEl;  // K (or V) of one stage
-  static constexpr int kStageBytes = 2 * kTileBytes;
-  static constexpr int kMinCtas = 3;
-  // the ring of a CTA: its share of the SM's shared memory, and the merge of the warps has to fit
-  static constexpr int kStages = 64 * 1024 / kStageBytes;
-  static constexpr int kRowPitch = D + 4;  // floats of a row in the merge: lanes' rows in different banks
-  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes;
-  static_assert(kConsumerWarps * kRows * (kRowPitch + 2) * 4 <= kStages * kStageBytes, "merge buffer");
+// The division of the work. A unit is one (sequence, kv head); its chunks are
+// KEYS keys each from MultiSeq::first on. The units' chunks, one after another
+// (the kv heads of sequence 0, of sequence 1, ...), are cut into even shares, one
+// per worker (CTA), so that the CTAs end together whatever the lengths. A worker
+// takes its share unit by unit: a unit that lies in one share is finished by its
+// worker; of a unit that does not, each worker leaves a partial (m, l, o): in
+// slot 2w if it is the worker's first segment, in slot 2w + 1 otherwise (it is
+// then the last), and the merge kernel folds them in order. The same lengths give
+// the same shares, so results do not change from call to call.
+constexpr int32_t kWholeUnits = INT32_MAX;
+
+struct MultiWork {
+  int32_t s, g, c;   // where the share starts: sequence, kv head, chunk of the unit
+  int64_t per;       // chunks of a share
+  int64_t left;      // chunks of this one, 0: none
 };
 
-// One group's scores of a warp's 16 keys (x: keys r, r + 8 of rows 2c, 2c + 1,
-// base 2, -inf where unseen) folded into its running state; leaves the weights
-// in x. The reference maximum moves only when a score exceeds it by 8, so
-// weights stay <= 2^8 and o is rarely rescaled.
-template <int DT>
-__device__ __forceinline__ void multi_softmax(float (&x)[4], float (&m_run)[2], float (&l_run)[2], float (&o)[DT][4]) {
-  float mloc[2];
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    float v = fmaxf(x[j], x[2 + j]);
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-    mloc[j] = v;
+// The share of worker w of `workers`, at least min_per chunks each; by one warp,
+// the same in every lane.
+template <int KEYS>
+__device__ __forceinline__ MultiWork find_work(const MultiArgs& a, int64_t w, int64_t workers, int min_per, bool report) {
+  const int lane = threadIdx.x & 31;
+  MultiWork k;
+  k.s = k.g = k.c = 0;
+  if (a.per == kWholeUnits) {
+    k.s = static_cast<int32_t>(w / a.hkv);
+    k.g = static_cast<int32_t>(w - static_cast<int64_t>(k.s) * a.hkv);
+    k.per = kWholeUnits;
+    k.left = load_multi_seq(a, k.s, report && k.g == 0 && lane == 0).chunks(KEYS);
+    return k;
   }
-  const bool move[2] = {mloc[0] > m_run[0] + 8.f, mloc[1] > m_run[1] + 8.f};
-  if (__any_sync(0xffffffffu, move[0] || move[1])) {
-    float alpha[2];
+  int64_t total = 0;
+  for (int s = lane; s < a.num_seqs; s += 32) total += load_multi_seq(a, s, report && w == 0).chunks(KEYS);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      alpha[j] = move[j] ? fast_exp2(m_run[j] - mloc[j]) : 1.f;  // 0 from -inf
-      if (move[j]) m_run[j] = mloc[j];
-      l_run[j] *= alpha[j];
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  total *= a.hkv;
+  k.per = a.per > 0 ? a.per : max(static_cast<int64_t>(min_per), (total + workers - 1) / workers);
+  const int64_t x = w * k.per;
+  k.left = x >= total ? 0 : min(k.per, total - x);
+  if (k.left == 0) return k;
+  int64_t base = 0;  // chunks (of one kv head) of the sequences before s0
+  for (int s0 = 0;; s0 += 32) {
+    const int c = s0 + lane < a.num_seqs ? load_multi_seq(a, s0 + lane, false).chunks(KEYS) : 0;
+    int64_t upto = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
     }
-#pragma unroll
-    for (int t = 0; t < DT; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[t][e] *= alpha[e & 1];
-  }
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const float ref = m_run[j] == -INFINITY ? 0.f : m_run[j];  // a row that has seen nothing: weights 0
-    x[j] = fast_exp2(x[j] - ref);
-    x[2 + j] = fast_exp2(x[2 + j] - ref);
-    l_run[j] += x[j] + x[2 + j];
+    const unsigned hit = __ballot_sync(0xffffffffu, (base + upto) * a.hkv > x);
+    if (hit) {
+      const int at = __ffs(hit) - 1;
+      const int64_t from = (base + __shfl_sync(0xffffffffu, upto - c, at)) * a.hkv;
+      const int cs = __shfl_sync(0xffffffffu, c, at);
+      k.s = s0 + at;
+      k.g = static_cast<int32_t>((x - from) / cs);
+      k.c = static_cast<int32_t>(x - from - static_cast<int64_t>(k.g) * cs);
+      return k;
+    }
+    base += __shfl_sync(0xffffffffu, upto, 31);
   }
 }
 
-template <int D, int NG, int CF>
-__global__ void __launch_bounds__(MultiCfg<D, NG, CF>::kThreads, MultiCfg<D, NG, CF>::kMinCtas)
+// One segment of a worker's share: some chunks of one unit.
+struct MultiSegment {
+  MultiSeq ms;
+  int32_t s, g, rows;
+  int32_t kbeg, kend;     // keys that some row sees, within the segment
+  int32_t begin, chunks;  // its first chunk's first key, and how many are read (0: no key to see)
+  bool whole;             // the whole unit
+  int64_t slot;           // of its partial otherwise
+};
+
+// Walks the segments of a share (every warp for itself).
+template <int KEYS>
+struct MultiWalk {
+  MultiWork k;
+  int64_t w;
+  bool started;
+  __device__ __forceinline__ MultiWalk(const MultiWork& work, int64_t worker) : k(work), w(worker), started(false) {}
+  __device__ __forceinline__ bool next(const MultiArgs& a, MultiSegment& e) {
+    if (k.left <= 0) return false;
+    int32_t cs;
+    for (;; ++k.s) {  // a share is left, so some sequence from here on has chunks
+      e.ms = load_multi_seq(a, k.s, false);
+      cs = e.ms.chunks(KEYS);
+      if (cs > 0) break;
+    }
+    const int32_t nc = static_cast<int32_t>(min(k.left, static_cast<int64_t>(cs - k.c)));
+    e.s = k.s;
+    e.g = k.g;
+    e.rows = e.ms.n << a.gshift;
+    e.begin = e.ms.first + k.c * KEYS;
+    e.kend = k.c + nc == cs ? e.ms.L : e.begin + nc * KEYS;
+    e.kbeg = max(e.begin, e.ms.L - e.ms.n - a.window + 1);
+    e.chunks = e.kend > e.kbeg ? (e.kend - e.begin + KEYS - 1) / KEYS : 0;
+    e.whole = k.c == 0 && nc == cs;
+    e.slot = 2 * w + (started ? 1 : 0);
+    started = true;
+    k.left -= nc;
+    k.c = 0;
+    if (++k.g == a.hkv) {
+      k.g = 0;
+      ++k.s;
+    }
+    return true;
+  }
+};
+
+// Row of q, out and lse of row rho of a segment.
+__device__ __forceinline__ int64_t multi_row(const MultiArgs& a, const MultiSegment& e, int rho) {
+  return static_cast<int64_t>(e.ms.q0 + (rho >> a.gshift)) * a.hq + (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1));
+}
+
+// Four dims d of row rho, from its (m, l) and unnormalised o: the result, or the
+// segment's partial.
+template <int D>
+__device__ __forceinline__ void store_multi(const MultiArgs& a, const MultiSegment& e, int rho, int d, float m, float l,
+                                            float4 o) {
+  if (!e.whole) {
+    const int64_t prow = e.slot * a.slot_rows + rho;
+    *reinterpret_cast<float4*>(a.ws_o + prow * D + d) = o;
+    if (d == 0) *reinterpret_cast<float2*>(a.ws_ml + prow * 2) = make_float2(m, l);
+    return;
+  }
+  float lse;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), m, l, lse) * a.v_scale;
+  const int64_t row = multi_row(a, e, rho);
+  const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * f, o.y * f), y1 = __floats2bfloat162_rn(o.z * f, o.w * f);
+  *reinterpret_cast<uint2*>(a.out + row * D + d) =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
+  if (d == 0 && a.lse) a.lse[row] = lse;
+}
+
+template <int D, int CF>
+struct MultiCfg {
+  static constexpr int kConsumerWarps = 4;
+  static constexpr int kThreads = 32 * (kConsumerWarps + 1);
+  static constexpr int kTiles = CF != 0 ? 2 : 1;   // 16-key MMA tiles of a warp per chunk
+  static constexpr int kChunk = 64 * kTiles;
+  static constexpr int kEl = CF != 0 ? 1 : 2;
+  static constexpr int kTileBytes = kChunk * D * kEl;  // K (or V) of one stage
+  static constexpr int kStageBytes = 2 * kTileBytes;
+  static constexpr int kCtas = 3;                  // per SM
+  static constexpr int kStages = 64 * 1024 / kStageBytes;
+  static constexpr int kFoldFloats = 32 * (D / 4 + 4);  // one warp's state
+  static constexpr int kRowPitch = D + 4;          // floats of a row of the result
+  static constexpr int kMinChunks = 256 / kChunk;  // of a share
+  static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 2 * kFoldFloats * 4;
+  static_assert(8 * (kRowPitch + 2) <= kFoldFloats, "the result takes the place of a state");
+};
+
+// Up to 8 rows. Warp 4 streams K/V into a ring of stages, on into the next
+// segment while the others finish one; warps 0-3 take 16 (8-bit: 32) keys each
+// of every chunk and fold their states in two rounds.
+template <int D, int CF>
+__global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kCtas)
     decode_multi_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                         const MultiArgs a) {
-  using Cfg = MultiCfg<D, NG, CF>;
-  constexpr int NW = Cfg::kConsumerWarps, C = Cfg::kChunk, S = Cfg::kStages, KS = D / 16;
+  using Cfg = MultiCfg<D, CF>;
+  constexpr int NW = Cfg::kConsumerWarps, C = Cfg::kChunk, S = Cfg::kStages, KS = D / 16, MT = Cfg::kTiles;
 
   extern __shared__ uint8_t smem_raw[];
   __shared__ PipeSmem<S> ps;
+  __shared__ int stop;
   const uint32_t sbase = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* sgen = smem_raw + (sbase - smem_u32(smem_raw));
+  float* fold = reinterpret_cast<float*>(sgen + S * Cfg::kStageBytes);
 
-  const int g = blockIdx.x, s = blockIdx.y;
-  const int p = blockIdx.z;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r = lane >> 2, c = lane & 3;
-  const MultiSeq ms = load_multi_seq(a, s, g == 0 && p == 0 && tid == 0);
-  const int rows = ms.n << a.gshift;
-  if (rows <= 0 || p >= ms.nparts) return;
-  // keys that some row sees, within the partition
-  const int32_t pos0 = ms.L - ms.n;  // position of the sequence's first new token
-  const int32_t pos_lo = pos0, pos_hi = pos0 + ms.n - 1;
-  const int32_t t0 = ms.nparts > 1 ? ms.first + p * a.part_tokens : 0;
-  const int32_t t1 = ms.nparts > 1 && p < ms.nparts - 1 ? t0 + a.part_tokens : ms.L;
-  const int32_t kbeg = max(t0, max(0, pos_lo - a.window + 1));
-  const int32_t kend = t1;
-  const int32_t c_begin = kbeg & ~(C - 1);
-  const int nchunks = kend > kbeg ? (kend - c_begin + C - 1) / C : 0;
-
-  TableAhead ta;
-  if (warp == NW)
-    ta.init(a.tables + static_cast<int64_t>(s) * a.max_blocks, c_begin / a.bs,
-            min(a.max_blocks, (kend + a.bs - 1) / a.bs), lane);
   if (tid == 0) {
     prefetch_tmap(&tmk);
     prefetch_tmap(&tmv);
     pipe_init<S>(ps, NW);
   }
-  // q as the B fragments of S^T (column r of group gi = row 8 gi + r, zeros
-  // past the last): dims (2c, 2c + 1) and (+8) of a 16-dim step, or
-  // over an 8-bit cache, as f16, dims (4c, 4c + 1) and (4c + 2, 4c + 3)
-  auto q_frag = [&](int gi, int kk) -> uint2 {
-    const int rho = 8 * gi + r;
-    if (rho >= rows) return make_uint2(0u, 0u);
-    const int64_t qrow = static_cast<int64_t>(ms.q0 + (rho >> a.gshift)) * a.hq + (g << a.gshift) +
-                         (rho & ((1 << a.gshift) - 1));
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(a.q + qrow * D) + kk * 8;
-    if constexpr (CF != 0) {
-      const uint2 x = *reinterpret_cast<const uint2*>(w + 2 * c);
-      return make_uint2(pack_f16(bf16lo(x.x), bf16hi(x.x)), pack_f16(bf16lo(x.y), bf16hi(x.y)));
-    } else {
-      return make_uint2(__ldg(w + c), __ldg(w + 4 + c));
-    }
-  };
-  uint2 qr[NG][KS];
-  if (warp < NW) {
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi)
-#pragma unroll
-      for (int kk = 0; kk < KS; ++kk) qr[gi][kk] = q_frag(gi, kk);
-  }
+  MultiWalk<C> walk(find_work<C>(a, blockIdx.x, gridDim.x, Cfg::kMinChunks, warp == 0), blockIdx.x);
+  MultiSegment e;
   __syncthreads();
 
-  float o[NG][KS][4], m_run[NG][2], l_run[NG][2];
-#pragma unroll
-  for (int gi = 0; gi < NG; ++gi) {
-    m_run[gi][0] = m_run[gi][1] = -INFINITY;
-    l_run[gi][0] = l_run[gi][1] = 0.f;
-#pragma unroll
-    for (int t = 0; t < KS; ++t) o[gi][t][0] = o[gi][t][1] = o[gi][t][2] = o[gi][t][3] = 0.f;
-  }
-
   if (warp == NW) {
-    // ---- producer: the blocks of chunk i that hold a key in [kbeg, kend) ----
+    // ---- producer: the blocks of every chunk that hold a key in [kbeg, kend) ----
     const uint32_t box_bytes = static_cast<uint32_t>(a.bs) * D * Cfg::kEl;
     const uint64_t pol = kv_stream_policy();
-    pipe_produce<S>(ps, nchunks, [&](int i, int st) {
-      const int32_t c0 = c_begin + i * C;
-      const int32_t nb = (min(C, kend - c0) + a.bs - 1) / a.bs;  // <= 8 (bs >= 8)
-      const int32_t blk = ta.get(c0 / a.bs, nb, lane);
-      bool ok = false;
-      if (lane < nb && c0 + (lane + 1) * a.bs > kbeg) {
-        ok = blk >= 0 && blk < a.num_blocks;
-        if (!ok) record_error(PA_ERR_DEVICE_BOUNDS, blk);
-      }
-      const unsigned okmask = __ballot_sync(0xffffffffu, ok);
-      if (lane == 0) mbar_arrive_expect_tx(&ps.full[st], 2u * __popc(okmask) * box_bytes);
-      __syncwarp();
-      if (ok) {
-        const int32_t y = (blk * a.hkv + g) * a.bs;
-        const uint32_t kdst = sbase + st * Cfg::kStageBytes + lane * box_bytes;
-        if constexpr (CF != 0) {
-          tma_load_2d(kdst, &tmk, 0, y, &ps.full[st], pol);
-          tma_load_2d(kdst + Cfg::kTileBytes, &tmv, 0, y, &ps.full[st], pol);
-        } else {
-          tma_block<D>(kdst, &tmk, y, &ps.full[st], pol);
-          tma_block<D>(kdst + Cfg::kTileBytes, &tmv, y, &ps.full[st], pol);
+    int jg = 0;
+    while (walk.next(a, e)) {
+      TableAhead ta;
+      ta.init(a.tables + static_cast<int64_t>(e.s) * a.max_blocks, e.begin / a.bs,
+              min(a.max_blocks, (e.kend + a.bs - 1) / a.bs), lane);
+      bool gave_up = false;
+      for (int j = 0; j < e.chunks; ++j, ++jg) {
+        const int st = jg % S;
+        if (jg >= S && !pipe_wait(&ps.empty[st], ((jg / S) - 1) & 1, &ps.abort_flag)) {
+          gave_up = true;
+          break;
         }
+        bool ok[MT];
+        int32_t blk[MT];
+        int cnt = 0;
+#pragma unroll
+        for (int u = 0; u < MT; ++u) {  // 64 keys at a time: at most 8 blocks (bs >= 8)
+          const int32_t h0 = e.begin + j * C + u * 64;
+          const int32_t nb = h0 < e.kend ? (min(64, e.kend - h0) + a.bs - 1) / a.bs : 0;
+          blk[u] = ta.get(h0 / a.bs, nb, lane);
+          ok[u] = false;
+          if (lane < nb && h0 + (lane + 1) * a.bs > e.kbeg) {
+            ok[u] = blk[u] >= 0 && blk[u] < a.num_blocks;
+            if (!ok[u]) record_error(PA_ERR_DEVICE_BOUNDS, blk[u]);
+          }
+          cnt += __popc(__ballot_sync(0xffffffffu, ok[u]));
+        }
+        if (lane == 0) mbar_arrive_expect_tx(&ps.full[st], 2u * cnt * box_bytes);
+        __syncwarp();
+#pragma unroll
+        for (int u = 0; u < MT; ++u)
+          if (ok[u]) {
+            const int32_t y = (blk[u] * a.hkv + e.g) * a.bs;
+            const uint32_t kdst = sbase + st * Cfg::kStageBytes + u * (64 * D * Cfg::kEl) + lane * box_bytes;
+            if constexpr (CF != 0) {
+              tma_load_2d(kdst, &tmk, 0, y, &ps.full[st], pol);
+              tma_load_2d(kdst + Cfg::kTileBytes, &tmv, 0, y, &ps.full[st], pol);
+            } else {
+              tma_block<D>(kdst, &tmk, y, &ps.full[st], pol);
+              tma_block<D>(kdst + Cfg::kTileBytes, &tmv, y, &ps.full[st], pol);
+            }
+          }
       }
-    });
+      if (gave_up) break;
+    }
+    if (ps.abort_flag)  // copies already started land before exit
+      for (int j = (jg > S ? jg - S : 0); j < jg; ++j) mbar_wait(&ps.full[j % S], (j / S) & 1);
   } else {
-    // ---- consumers: warp w has keys [16w, 16w + 16) of every chunk ----
-    // positions of this lane's rows 8 gi + 2c + j: the last key each sees
-    int32_t pos[NG][2];
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = 8 * gi + 2 * c + j;
-        pos[gi][j] = row < rows ? pos0 + (row >> a.gshift) : -1;
-      }
+    // ---- consumers: warp w has keys [16 MT w, 16 MT (w + 1)) of every chunk ----
     const int mk = lane >> 3, ik = lane & 7;
-    for (int i = 0; i < nchunks; ++i) {
-      const int st = i % S;
-      if (!pipe_wait(&ps.full[st], (i / S) & 1, &ps.abort_flag)) break;
-      const int32_t key0 = c_begin + i * C + warp * 16;  // this warp's first key
-      if (key0 + 16 > kbeg && key0 < kend) {             // warp-uniform
-        const uint32_t kst = sbase + st * Cfg::kStageBytes, vst = kst + Cfg::kTileBytes;
-        float x[NG][4];
-        if constexpr (CF == 0) {
-          // stage layout as in mma_chunk: block-major, 64-element halves, swizzled rows
-          const int tokK = warp * 16 + (mk >> 1) * 8 + ik, dK = (mk & 1) * 8;
-          const uint32_t hstride = static_cast<uint32_t>(a.bs) * 128u;
-          const uint32_t kbase = kst + (tokK + (tokK & ~(a.bs - 1)) * (D / 64 - 1)) * 128;
-          float s1[NG == 1 ? 4 : 1] = {};
+    int jg = 0;
+    while (walk.next(a, e)) {
+      const int32_t pos0 = e.ms.L - e.ms.n, pos_hi = e.ms.L - 1;  // positions of the first and last new token
+      // q as the B fragments of S^T (column r = row r, zeros past the last): dims
+      // (2c, 2c + 1) and (+8) of a 16-dim step, or over an 8-bit cache, as f16,
+      // dims (4c, 4c + 1) and (4c + 2, 4c + 3)
+      uint2 qr[KS];
+      {
+        const uint32_t* w = reinterpret_cast<const uint32_t*>(a.q + multi_row(a, e, r < e.rows ? r : 0) * D);
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi) x[gi][0] = x[gi][1] = x[gi][2] = x[gi][3] = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            const int d0 = kk * 16 + dK;
-            uint32_t m0, m1, m2, m3;
-            ldsm_x4(kbase + (d0 >> 6) * hstride + ((((d0 & 63) >> 3) ^ (tokK & 7)) << 4), m0, m1, m2, m3);
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              const uint2 qq = qr[gi][kk];
-              if constexpr (NG == 1)
-                mma16x8(kk & 1 ? s1 : x[gi], m0, m2, m1, m3, qq.x, qq.y);  // two chains
-              else
-                mma16x8(x[gi], m0, m2, m1, m3, qq.x, qq.y);
+        for (int kk = 0; kk < KS; ++kk) {
+          qr[kk] = make_uint2(0u, 0u);
+          if (r < e.rows) {
+            if constexpr (CF != 0) {
+              const uint2 x = __ldg(reinterpret_cast<const uint2*>(w + kk * 8 + 2 * c));
+              qr[kk] = make_uint2(pack_f16(bf16lo(x.x), bf16hi(x.x)), pack_f16(bf16lo(x.y), bf16hi(x.y)));
+            } else {
+              qr[kk] = make_uint2(__ldg(w + kk * 8 + c), __ldg(w + kk * 8 + 4 + c));
             }
           }
-          if constexpr (NG == 1)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[0][e] += s1[e];
-        } else {
-          uint32_t rb[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const int row = warp * 16 + h * 8 + r;
-            const uint32_t key = D == 128 ? static_cast<uint32_t>(row & 7) : static_cast<uint32_t>((row >> 1) & 3);
-            rb[h] = (kst + static_cast<uint32_t>(row * D)) | (key << 4) | static_cast<uint32_t>(4 * c);
-          }
-          float s1[NG == 1 ? 4 : 1] = {};
-#pragma unroll
-          for (int gi = 0; gi < NG; ++gi) x[gi][0] = x[gi][1] = x[gi][2] = x[gi][3] = 0.f;
-#pragma unroll
-          for (int kk = 0; kk < KS; ++kk) {
-            uint32_t w0, w1;
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(rb[0] ^ static_cast<uint32_t>(kk << 4)));
-            asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(rb[1] ^ static_cast<uint32_t>(kk << 4)));
-            uint32_t k00, k01, k10, k11;
-            widen4<CF>(w0, k00, k01);
-            widen4<CF>(w1, k10, k11);
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              const uint2 qq = qr[gi][kk];
-              if constexpr (NG == 1)
-                mma16x8_f16(kk & 1 ? s1 : x[gi], k00, k10, k01, k11, qq.x, qq.y);
-              else
-                mma16x8_f16(x[gi], k00, k10, k01, k11, qq.x, qq.y);
-            }
-          }
-          if constexpr (NG == 1)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[0][e] += s1[e];
         }
-        // base-2 scores; -inf outside a row's keys (every row sees all 16 keys
-        // in most chunks). A key past kend is past its row's position
-        // or in the next partition, one before kbeg before every window.
-        if (a.cap_log2 > 0.f) {
+      }
+      // positions of this lane's rows 2c, 2c + 1: the last key each sees
+      int32_t pos[2];
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi)
+      for (int j = 0; j < 2; ++j) pos[j] = 2 * c + j < e.rows ? pos0 + ((2 * c + j) >> a.gshift) : -1;
+      float o[KS][4], m_run[2] = {-INFINITY, -INFINITY}, l_run[2] = {0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[gi][e] = capped_score(x[gi][e] * a.cap_arg, a.cap_log2);
-        } else {
+      for (int t = 0; t < KS; ++t) o[t][0] = o[t][1] = o[t][2] = o[t][3] = 0.f;
+
+      for (int j = 0; j < e.chunks; ++j, ++jg) {
+        const int st = jg % S;
+        if (!pipe_wait(&ps.full[st], (jg / S) & 1, &ps.abort_flag)) break;
+        const int32_t key0 = e.begin + j * C + warp * (16 * MT);  // this warp's first key
+        if (key0 + 16 * MT > e.kbeg && key0 < e.kend) {           // warp-uniform
+          const uint32_t kst = sbase + st * Cfg::kStageBytes, vst = kst + Cfg::kTileBytes;
+          float x[MT][4];  // scores of keys r, r + 8 of a tile, rows 2c, 2c + 1; two chains
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi)
+          for (int u = 0; u < MT; ++u) {
+            float s1[4] = {0.f, 0.f, 0.f, 0.f};
+            x[u][0] = x[u][1] = x[u][2] = x[u][3] = 0.f;
+            if constexpr (CF == 0) {
+              // stage layout as in mma_chunk: block-major, 64-element halves, swizzled rows
+              const int tok = warp * 16 + (mk >> 1) * 8 + ik, dK = (mk & 1) * 8;
+              const uint32_t hstride = static_cast<uint32_t>(a.bs) * 128u;
+              const uint32_t kbase = kst + (tok + (tok & ~(a.bs - 1)) * (D / 64 - 1)) * 128;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[gi][e] *= a.scale_log2;
-        }
-        const bool inside = key0 >= kbeg && key0 + 16 <= kend;
-        if (!inside || key0 + 15 > pos_lo || key0 <= pos_hi - a.window) {
+              for (int kk = 0; kk < KS; ++kk) {
+                const int d0 = kk * 16 + dK;
+                uint32_t m0, m1, m2, m3;
+                ldsm_x4(kbase + (d0 >> 6) * hstride + ((((d0 & 63) >> 3) ^ (tok & 7)) << 4), m0, m1, m2, m3);
+                mma16x8(kk & 1 ? s1 : x[u], m0, m2, m1, m3, qr[kk].x, qr[kk].y);
+              }
+            } else {
+              uint32_t rb[2];
 #pragma unroll
-          for (int gi = 0; gi < NG; ++gi)
+              for (int h = 0; h < 2; ++h) {
+                const int row = (warp * MT + u) * 16 + h * 8 + r;
+                const uint32_t key = D == 128 ? static_cast<uint32_t>(row & 7) : static_cast<uint32_t>((row >> 1) & 3);
+                rb[h] = (kst + static_cast<uint32_t>(row * D)) | (key << 4) | static_cast<uint32_t>(4 * c);
+              }
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int32_t key = key0 + r + (e >> 1) * 8, ps_ = pos[gi][e & 1];
-              if (key < kbeg || key >= kend || key > ps_ || key <= ps_ - a.window) x[gi][e] = -INFINITY;
-            }
-        }
-        // weights, and P^T as B fragments (K 16 keys x N 8 rows)
-        uint32_t pb[NG][CF != 0 ? 2 : 4];
-#pragma unroll
-        for (int gi = 0; gi < NG; ++gi) {
-          multi_softmax<KS>(x[gi], m_run[gi], l_run[gi], o[gi]);
-          if constexpr (CF != 0) {
-            pb[gi][0] = movmatrix_t(pack_f16(x[gi][0], x[gi][1]));
-            pb[gi][1] = movmatrix_t(pack_f16(x[gi][2], x[gi][3]));
-          } else {
-            uint32_t h01, l01, h23, l23;
-            split_pair(x[gi][0], x[gi][1], h01, l01);
-            split_pair(x[gi][2], x[gi][3], h23, l23);
-            pb[gi][0] = movmatrix_t(h01);
-            pb[gi][1] = movmatrix_t(h23);
-            pb[gi][2] = movmatrix_t(l01);
-            pb[gi][3] = movmatrix_t(l23);
-          }
-        }
-        // V rows outside [kbeg, kend) as zeros: this lane's keys 2c, 2c + 1 (mlo) and + 8 (mhi)
-        uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
-        if (!inside) {
-          auto live = [&](int k) { return key0 + k >= kbeg && key0 + k < kend; };
-          mlo = (live(2 * c) ? 0x0000ffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
-          mhi = (live(2 * c + 8) ? 0x0000ffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
-        }
-        if constexpr (CF == 0) {
-          const int tokV = warp * 16 + (mk & 1) * 8 + ik, dV = (mk >> 1) * 8;
-          const uint32_t hstride = static_cast<uint32_t>(a.bs) * 128u;
-          const uint32_t vbase = vst + (tokV + (tokV & ~(a.bs - 1)) * (D / 64 - 1)) * 128;
-#pragma unroll
-          for (int t = 0; t < KS; ++t) {
-            const int d0 = t * 16 + dV;
-            uint32_t v0, v1, v2, v3;
-            ldsm_x4_t(vbase + (d0 >> 6) * hstride + ((((d0 & 63) >> 3) ^ (tokV & 7)) << 4), v0, v1, v2, v3);
-            v0 &= mlo;
-            v1 &= mhi;
-            v2 &= mlo;
-            v3 &= mhi;
-#pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              mma16x8(o[gi][t], v0, v2, v1, v3, pb[gi][0], pb[gi][1]);
-              mma16x8(o[gi][t], v0, v2, v1, v3, pb[gi][2], pb[gi][3]);
-            }
-          }
-        } else {
-          constexpr int W = D == 128 ? 4 : 2;  // 32-bit words of V per key this thread reads
-          const uint8_t* vt = sgen + (vst - sbase);
-          const int col = f8_dim<D>(0, r), ta0 = warp * 16 + 2 * c, tb0 = ta0 + 8;
-          const uint8_t* pa_ = vt + f8_off<D>(ta0, col);
-          const uint8_t* pb_ = vt + f8_off<D>(ta0 + 1, col);
-          const uint8_t* pc_ = vt + f8_off<D>(tb0, col);
-          const uint8_t* pd_ = vt + f8_off<D>(tb0 + 1, col);
-#pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const uint32_t xa = *reinterpret_cast<const uint32_t*>(pa_ + 4 * w);
-            const uint32_t xb = *reinterpret_cast<const uint32_t*>(pb_ + 4 * w);
-            const uint32_t xc = *reinterpret_cast<const uint32_t*>(pc_ + 4 * w);
-            const uint32_t xd = *reinterpret_cast<const uint32_t*>(pd_ + 4 * w);
-            uint32_t b[8];
-            widen4<CF>(__byte_perm(xa, xb, 0x5140), b[0], b[1]);
-            widen4<CF>(__byte_perm(xa, xb, 0x7362), b[2], b[3]);
-            widen4<CF>(__byte_perm(xc, xd, 0x5140), b[4], b[5]);
-            widen4<CF>(__byte_perm(xc, xd, 0x7362), b[6], b[7]);
-            if (!inside) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                b[k] &= mlo;
-                b[4 + k] &= mhi;
+              for (int kk = 0; kk < KS; ++kk) {
+                uint32_t w0, w1;
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w0) : "r"(rb[0] ^ static_cast<uint32_t>(kk << 4)));
+                asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w1) : "r"(rb[1] ^ static_cast<uint32_t>(kk << 4)));
+                uint32_t k00, k01, k10, k11;
+                widen4<CF>(w0, k00, k01);
+                widen4<CF>(w1, k10, k11);
+                mma16x8_f16(kk & 1 ? s1 : x[u], k00, k10, k01, k11, qr[kk].x, qr[kk].y);
               }
             }
 #pragma unroll
-            for (int gi = 0; gi < NG; ++gi) {
-              mma16x8_f16(o[gi][2 * w], b[0], b[1], b[4], b[5], pb[gi][0], pb[gi][1]);
-              mma16x8_f16(o[gi][2 * w + 1], b[2], b[3], b[6], b[7], pb[gi][0], pb[gi][1]);
+            for (int i = 0; i < 4; ++i) x[u][i] += s1[i];
+          }
+          // base-2 scores; -inf outside a row's keys (every row sees all of the
+          // warp's keys in most chunks)
+          if (a.cap_log2 > 0.f) {
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[u][i] = capped_score(x[u][i] * a.cap_arg, a.cap_log2);
+          } else {
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[u][i] *= a.scale_log2;
+          }
+          const bool inside = key0 >= e.kbeg && key0 + 16 * MT <= e.kend;
+          if (!inside || key0 + 16 * MT - 1 > pos0 || key0 <= pos_hi - a.window) {
+#pragma unroll
+            for (int u = 0; u < MT; ++u)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int32_t key = key0 + u * 16 + r + (i >> 1) * 8, last = pos[i & 1];
+                if (key < e.kbeg || key >= e.kend || key > last || key <= last - a.window) x[u][i] = -INFINITY;
+              }
+          }
+          // weights. The reference maximum moves only when a score exceeds it by
+          // 8, so weights stay <= 2^8 and o is rarely rescaled
+          float mloc[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v = fmaxf(x[0][h], x[0][2 + h]);
+            if constexpr (MT == 2) v = fmax3(v, x[1][h], x[1][2 + h]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            mloc[h] = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+          }
+          const bool move[2] = {mloc[0] > m_run[0] + 8.f, mloc[1] > m_run[1] + 8.f};
+          if (__any_sync(0xffffffffu, move[0] || move[1])) {
+            float alpha[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              alpha[h] = move[h] ? fast_exp2(m_run[h] - mloc[h]) : 1.f;  // 0 from -inf
+              if (move[h]) m_run[h] = mloc[h];
+              l_run[h] *= alpha[h];
+            }
+#pragma unroll
+            for (int t = 0; t < KS; ++t)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[t][i] *= alpha[i & 1];
+          }
+          // P^T as B fragments (K 16 keys x N 8 rows): f16, or over a bf16 cache a
+          // bf16 and its remainder
+          uint32_t pb[MT][CF != 0 ? 2 : 4];
+          const float ref[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0],   // a row that has seen
+                                m_run[1] == -INFINITY ? 0.f : m_run[1]};  // nothing: weights 0
+#pragma unroll
+          for (int u = 0; u < MT; ++u) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) x[u][i] = fast_exp2(x[u][i] - ref[i & 1]);
+            l_run[0] += x[u][0] + x[u][2];
+            l_run[1] += x[u][1] + x[u][3];
+            if constexpr (CF != 0) {
+              pb[u][0] = movmatrix_t(pack_f16(x[u][0], x[u][1]));
+              pb[u][1] = movmatrix_t(pack_f16(x[u][2], x[u][3]));
+            } else {
+              uint32_t h01, l01, h23, l23;
+              split_pair(x[u][0], x[u][1], h01, l01);
+              split_pair(x[u][2], x[u][3], h23, l23);
+              pb[u][0] = movmatrix_t(h01);
+              pb[u][1] = movmatrix_t(h23);
+              pb[u][2] = movmatrix_t(l01);
+              pb[u][3] = movmatrix_t(l23);
+            }
+          }
+          // V rows outside [kbeg, kend) as zeros: this lane's keys 2c, 2c + 1 (mlo) and + 8 (mhi)
+#pragma unroll
+          for (int u = 0; u < MT; ++u) {
+            uint32_t mlo = 0xffffffffu, mhi = 0xffffffffu;
+            if (!inside) {
+              auto live = [&](int k) {
+                return key0 + u * 16 + k >= e.kbeg && key0 + u * 16 + k < e.kend;
+              };
+              mlo = (live(2 * c) ? 0x0000ffffu : 0u) | (live(2 * c + 1) ? 0xffff0000u : 0u);
+              mhi = (live(2 * c + 8) ? 0x0000ffffu : 0u) | (live(2 * c + 9) ? 0xffff0000u : 0u);
+            }
+            if constexpr (CF == 0) {
+              const int tok = warp * 16 + (mk & 1) * 8 + ik, dV = (mk >> 1) * 8;
+              const uint32_t hstride = static_cast<uint32_t>(a.bs) * 128u;
+              const uint32_t vbase = vst + (tok + (tok & ~(a.bs - 1)) * (D / 64 - 1)) * 128;
+#pragma unroll
+              for (int t = 0; t < KS; ++t) {
+                const int d0 = t * 16 + dV;
+                uint32_t v0, v1, v2, v3;
+                ldsm_x4_t(vbase + (d0 >> 6) * hstride + ((((d0 & 63) >> 3) ^ (tok & 7)) << 4), v0, v1, v2, v3);
+                v0 &= mlo;
+                v1 &= mhi;
+                v2 &= mlo;
+                v3 &= mhi;
+                mma16x8(o[t], v0, v2, v1, v3, pb[u][0], pb[u][1]);
+                mma16x8(o[t], v0, v2, v1, v3, pb[u][2], pb[u][3]);
+              }
+            } else {
+              constexpr int W = D == 128 ? 4 : 2;  // 32-bit words of V per key this thread reads
+              const uint8_t* vt = sgen + (vst - sbase);
+              const int col = f8_dim<D>(0, r), ta0 = (warp * MT + u) * 16 + 2 * c, tb0 = ta0 + 8;
+              const uint8_t* pa_ = vt + f8_off<D>(ta0, col);
+              const uint8_t* pb_ = vt + f8_off<D>(ta0 + 1, col);
+              const uint8_t* pc_ = vt + f8_off<D>(tb0, col);
+              const uint8_t* pd_ = vt + f8_off<D>(tb0 + 1, col);
+#pragma unroll
+              for (int w = 0; w < W; ++w) {
+                const uint32_t xa = *reinterpret_cast<const uint32_t*>(pa_ + 4 * w);
+                const uint32_t xb = *reinterpret_cast<const uint32_t*>(pb_ + 4 * w);
+                const uint32_t xc = *reinterpret_cast<const uint32_t*>(pc_ + 4 * w);
+                const uint32_t xd = *reinterpret_cast<const uint32_t*>(pd_ + 4 * w);
+                uint32_t b[8];
+                widen4<CF>(__byte_perm(xa, xb, 0x5140), b[0], b[1]);
+                widen4<CF>(__byte_perm(xa, xb, 0x7362), b[2], b[3]);
+                widen4<CF>(__byte_perm(xc, xd, 0x5140), b[4], b[5]);
+                widen4<CF>(__byte_perm(xc, xd, 0x7362), b[6], b[7]);
+                if (!inside) {
+#pragma unroll
+                  for (int k = 0; k < 4; ++k) {
+                    b[k] &= mlo;
+                    b[4 + k] &= mhi;
+                  }
+                }
+                mma16x8_f16(o[2 * w], b[0], b[1], b[4], b[5], pb[u][0], pb[u][1]);
+                mma16x8_f16(o[2 * w + 1], b[2], b[3], b[6], b[7], pb[u][0], pb[u][1]);
+              }
             }
           }
         }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ps.empty[st]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ps.empty[st]);
-    }
+      sum_l(l_run);
+      // fold the warps' states: 2 and 3 into 0 and 1, 1 into 0, then out as rows. A
+      // warp that gave up a wait joins every barrier; thread 0 decides for all.
+      float* mine = fold + (warp & 1) * Cfg::kFoldFloats + lane * (D / 4 + 4);
+      if (warp >= 2) store_state<D>(mine, m_run, l_run, o);
+      consumer_bar();
+      if (warp < 2) fold_state<D>(m_run, l_run, o, mine);
+      consumer_bar();
+      if (warp == 1) store_state<D>(fold + lane * (D / 4 + 4), m_run, l_run, o);
+      consumer_bar();
+      float* rowsf = fold + Cfg::kFoldFloats;
+      float* ml = rowsf + 8 * Cfg::kRowPitch;
+      if (warp == 0) {
+        fold_state<D>(m_run, l_run, o, fold + lane * (D / 4 + 4));
 #pragma unroll
-    for (int gi = 0; gi < NG; ++gi) sum_l(l_run[gi]);
+        for (int h = 0; h < 2; ++h) {
+          float* dst = rowsf + (2 * c + h) * Cfg::kRowPitch;
+#pragma unroll
+          for (int t = 0; t < KS; ++t) {
+            dst[CF != 0 ? f8_dim<D>(t, r) : 16 * t + r] = o[t][h];
+            dst[CF != 0 ? f8_dim<D>(t, r) + 1 : 16 * t + r + 8] = o[t][2 + h];
+          }
+          if (r == 0) {
+            ml[2 * (2 * c + h)] = m_run[h];
+            ml[2 * (2 * c + h) + 1] = l_run[h];
+          }
+        }
+        if (lane == 0) stop = *static_cast<volatile int*>(&ps.abort_flag);
+      }
+      consumer_bar();
+      if (stop) break;
+      for (int i = tid; i < e.rows * (D / 4); i += 32 * NW) {
+        const int rho = i / (D / 4), d = (i - rho * (D / 4)) * 4;
+        store_multi<D>(a, e, rho, d, ml[2 * rho], ml[2 * rho + 1],
+                       *reinterpret_cast<const float4*>(rowsf + rho * Cfg::kRowPitch + d));
+      }
+      consumer_bar();  // the buffer is free for the next segment
+    }
   }
-
   pdl_launch_dependents();
-  __syncthreads();  // every copy consumed; the stage ring is free
-  if (ps.abort_flag) return;
-
-  // merge of the warps: wm, wl [NW][rows], wacc [NW][rows][pitch]
-  constexpr int RT = Cfg::kRows, RP = Cfg::kRowPitch;
-  float* wacc = reinterpret_cast<float*>(sgen);
-  float* wm = wacc + NW * RT * RP;
-  float* wl = wm + NW * RT;
-  if (warp < NW) {
-#pragma unroll
-    for (int gi = 0; gi < NG; ++gi)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int row = 8 * gi + 2 * c + j;
-        if (r == 0) {
-          wm[warp * RT + row] = m_run[gi][j];
-          wl[warp * RT + row] = l_run[gi][j];
-        }
-        float* dst = wacc + (warp * RT + row) * RP;
-#pragma unroll
-        for (int t = 0; t < KS; ++t) {
-          dst[CF != 0 ? f8_dim<D>(t, r) : 16 * t + r] = o[gi][t][j];
-          dst[CF != 0 ? f8_dim<D>(t, r) + 1 : 16 * t + r + 8] = o[gi][t][2 + j];
-        }
-      }
-  }
-  __syncthreads();
-  for (int idx = tid; idx < rows * (D / 4); idx += Cfg::kThreads) {
-    const int row = idx / (D / 4), d = (idx - row * (D / 4)) * 4;
-    float M = -INFINITY;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, wm[w * RT + row]);
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (M != -INFINITY) {
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float f = exp2f(wm[w * RT + row] - M);
-        const float4 v = *reinterpret_cast<const float4*>(wacc + (w * RT + row) * RP + d);
-        l = fmaf(wl[w * RT + row], f, l);
-        acc.x = fmaf(v.x, f, acc.x);
-        acc.y = fmaf(v.y, f, acc.y);
-        acc.z = fmaf(v.z, f, acc.z);
-        acc.w = fmaf(v.w, f, acc.w);
-      }
-    }
-    const int h = (g << a.gshift) + (row & ((1 << a.gshift) - 1));
-    const int64_t orow = static_cast<int64_t>(ms.q0 + (row >> a.gshift)) * a.hq + h;
-    if (ms.nparts > 1) {
-      const int64_t prow = orow * a.max_parts + p;
-      *reinterpret_cast<float4*>(a.ws_o + prow * D + d) = acc;
-      if (d == 0) *reinterpret_cast<float2*>(a.ws_ml + prow * 2) = make_float2(M, l);
-      continue;
-    }
-    float lse;
-    const float f = finish_row(a.sinks, h, M, l, lse) * a.v_scale;
-    const __nv_bfloat162 y0 = __floats2bfloat162_rn(acc.x * f, acc.y * f), y1 = __floats2bfloat162_rn(acc.z * f, acc.w * f);
-    *reinterpret_cast<uint2*>(a.out + orow * D + d) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
-    if (d == 0 && a.lse) a.lse[orow] = lse;
-  }
 }
 
-// Merge of a split sequence's partials: one warp per (new token, query head)
-// row, grid (rows of the longest sequence / warps, sequences). A lane owns D / 32
-// dims, so a partial is one coalesced read; four are in flight at a time.
+// Merge of the units that several workers share: CTA row w looks at the boundary
+// between workers w - 1 and w (grid.x: w from 1, grid.y: rows, a warp each). The
+// first boundary inside a unit merges it, over the partials of worker w - 1 and of
+// those from w on until the unit's end.
 constexpr int kMultiMergeWarps = 4;
 
-template <int D>
+template <int D, int KEYS, int MIN_CHUNKS>
 __global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kernel(const MultiArgs a) {
   constexpr int VEC = D / 32, U = 4;
-  const int s = blockIdx.y, lane = threadIdx.x & 31;
-  const int ri = blockIdx.x * kMultiMergeWarps + (threadIdx.x >> 5);
-  const MultiSeq ms = load_multi_seq(a, s, false);
+  const int lane = threadIdx.x & 31;
+  const int rho = blockIdx.y * kMultiMergeWarps + (threadIdx.x >> 5);
+  const int64_t w = blockIdx.x + 1;
+  const MultiWork k = find_work<KEYS>(a, w, gridDim.x + 1, MIN_CHUNKS, false);
+  MultiSegment e;
+  e.s = k.s;
+  e.g = k.g;
+  e.ms = load_multi_seq(a, k.s, false);
+  e.rows = e.ms.n << a.gshift;
+  e.whole = true;
+  e.slot = 0;
   pdl_wait();  // the partials are written by the grid this one was launched behind
-  if (ms.nparts <= 1 || ri >= ms.n * a.hq) return;
-  const int64_t row = static_cast<int64_t>(ms.q0) * a.hq + ri;
-  const float* ml = a.ws_ml + row * a.max_parts * 2;
-  const float* po = a.ws_o + row * a.max_parts * D + lane * VEC;
+  if (k.left == 0 || k.c == 0 || k.c > k.per || rho >= e.rows) return;
+  // worker w - 1 has the first k.c chunks (in its slot 0 if they are all it has),
+  // the workers from w on the rest
+  const int32_t rest = e.ms.chunks(KEYS) - k.c;
+  const int nparts = 1 + static_cast<int>((rest + k.per - 1) / k.per);
+  auto slot = [&](int q) { return (q == 0 ? 2 * (w - 1) + (k.c == k.per ? 0 : 1) : 2 * (w + q - 1)) * a.slot_rows + rho; };
   float M = -INFINITY;
-  for (int q = lane; q < ms.nparts; q += 32) M = fmaxf(M, __ldcg(ml + 2 * q));
+  for (int q = lane; q < nparts; q += 32) M = fmaxf(M, __ldcg(a.ws_ml + 2 * slot(q)));
   M = warp_max(M);
   float l = 0.f, acc[VEC];
 #pragma unroll
-  for (int e = 0; e < VEC; ++e) acc[e] = 0.f;
+  for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   if (M != -INFINITY) {
-    for (int q0 = 0; q0 < ms.nparts; q0 += U) {
+    for (int q0 = 0; q0 < nparts; q0 += U) {  // U partials in flight at a time
       float f[U], lq[U], x[U][VEC];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int q = min(q0 + u, ms.nparts - 1);
-        f[u] = __ldcg(ml + 2 * q);
-        lq[u] = __ldcg(ml + 2 * q + 1);
+        const int64_t row = slot(min(q0 + u, nparts - 1));
+        f[u] = __ldcg(a.ws_ml + 2 * row);
+        lq[u] = __ldcg(a.ws_ml + 2 * row + 1);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) x[u][e] = __ldcg(po + static_cast<int64_t>(q) * D + e);
+        for (int i = 0; i < VEC; ++i) x[u][i] = __ldcg(a.ws_o + row * D + lane * VEC + i);
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float w = q0 + u < ms.nparts ? exp2f(f[u] - M) : 0.f;
-        l = fmaf(lq[u], w, l);
+        const float wt = q0 + u < nparts ? exp2f(f[u] - M) : 0.f;
+        l = fmaf(lq[u], wt, l);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) acc[e] = fmaf(x[u][e], w, acc[e]);
+        for (int i = 0; i < VEC; ++i) acc[i] = fmaf(x[u][i], wt, acc[i]);
       }
     }
   }
   float lse;
-  const float f = finish_row(a.sinks, ri % a.hq, M, l, lse) * a.v_scale;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), M, l, lse) * a.v_scale;
+  const int64_t row = multi_row(a, e, rho);
   __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * VEC);
 #pragma unroll
-  for (int e = 0; e < VEC / 2; ++e) dst[e] = __floats2bfloat162_rn(acc[2 * e] * f, acc[2 * e + 1] * f);
+  for (int i = 0; i < VEC / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * f, acc[2 * i + 1] * f);
   if (lane == 0 && a.lse) a.lse[row] = lse;
 }
 

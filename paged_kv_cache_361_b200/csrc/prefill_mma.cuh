@@ -56,9 +56,11 @@ struct PrefillArgs {
   float* lse = nullptr;            // [num_tokens][hq] or null
   const float* sinks = nullptr;    // [hq] or null
   int32_t num_tokens = 0, max_q = 0;
+  int32_t gshift = 0;              // log2 of hq / hkv
   int32_t window = 0;              // >= 1; max_ctx or more: every earlier key
   float cap_log2 = 0.f;            // softcap * log2 e, 0: none
-  float cap_arg = 0.f;             // with a cap: 2 log2 e * scale / softcap (times the K scale)
+  float cap_k = 0.f;               // with a cap: scale / softcap (times the K scale)
+  float cap_arg = 0.f;             // 2 log2 e * cap_k
 };
 
 // d += A(16x16) * B(16x8), all 16 rows live.

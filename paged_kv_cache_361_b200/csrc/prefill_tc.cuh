@@ -162,6 +162,7 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 // TILES query tiles of one (kv head, sequence) per CTA share the K/V stream;
 // tile t is processed by softmax warpgroup t.
 // CF = 0: bf16 cache; kCodeE4M3 / kCodeS8: an 8-bit cache of that format.
+// G: query heads of a kv head (OPT: 0, it is an argument).
 template <int D, int G, int TILES, int CF = 0, bool OPT = false>
 __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -169,7 +170,12 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
                       const PrefillArgs a) {
   constexpr bool F8 = CF != 0;
   using Cfg = TcCfg<D, TILES, F8>;
-  constexpr int S = Cfg::kStages, C = Cfg::kChunk, TT = Cfg::kRows / G;
+  constexpr int S = Cfg::kStages, C = Cfg::kChunk;
+  static_assert(G > 0 || OPT, "the group size is an argument in the OPT form alone");
+  const int GG = G > 0 ? G : 1 << a.gshift;   // query heads of a kv head
+  const int TT = G > 0 ? Cfg::kRows / (G > 0 ? G : 1) : Cfg::kRows >> a.gshift;             // tokens of a tile
+  auto tok_of = [&](int row) { return G > 0 ? row / (G > 0 ? G : 1) : row >> a.gshift; };
+  auto head_of = [&](int row) { return G > 0 ? row % (G > 0 ? G : 1) : row & (GG - 1); };
   constexpr int CS = F8 ? Cfg::kCodeStages : 1;
 
   extern __shared__ uint8_t smem_raw[];
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         if (q_by_tma(t)) {
 #pragma unroll
           for (int hf = 0; hf < Cfg::kHalves; ++hf)
-            tma_load_3d(sbase + t * Cfg::kQTileBytes + hf * Cfg::kQHalfBytes, &tmq, hf * 64, g * G,
+            tma_load_3d(sbase + t * Cfg::kQTileBytes + hf * Cfg::kQHalfBytes, &tmq, hf * 64, g * GG,
                         q0 + tok00 + t * TT, &q_full, pol);
         }
     }
@@ -506,11 +512,11 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     const int32_t kfirst = (c_first + jb[t]) * C;
     if (mych > 0) {
       const int32_t tok_end = min(tok0 + TT, n);
-      const int tok = tok0 + r / G;
+      const int tok = tok0 + tok_of(r);
       const bool valid = tok < n;
       const int32_t pos = base + (valid ? tok : tok_end - 1);  // last key the row sees
-      const int h = r % G;
-      const int64_t orow = (static_cast<int64_t>(q0) + (valid ? tok : 0)) * a.hq + g * G + h;
+      const int h = head_of(r);
+      const int64_t orow = (static_cast<int64_t>(q0) + (valid ? tok : 0)) * a.hq + g * GG + h;
       if (!q_by_tma(t)) {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + orow * D);
         uint8_t* qdst = sgen + t * Cfg::kQTileBytes;
@@ -532,7 +538,8 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         if (lane == 0) mbar_arrive(&q_full);
       }
       const uint32_t trow = tmem + t * Cfg::kTileCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-      const float sl2 = OPT && a.cap_log2 > 0.f ? 1.f : a.scale_log2;  // capped scores are in base 2 already
+      const float sl2 = a.scale_log2;
+      const CapPoly poly(OPT ? a.cap_log2 : 0.f);
       float m_ref = -INFINITY, l = 0.f;  // m_ref in scaled (log2) units
       bool ok = true;
       for (int j = 0; j < mych; ++j) {
@@ -547,20 +554,9 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         tc::ld32(trow + D + sb * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tc::wait_ld();
         const int32_t k0 = kfirst + j * C;
+        const float amax = OPT && a.cap_log2 > 0.f ? row_amax(sr) : 0.f;
         float x[C];
-        // the row maximum over 4 independent partial maxima (three-input max:
-        // short dependence chains, one instruction per two scores)
-        float pm[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) pm[u] = -INFINITY;
         // warp-uniform choice: tcgen05.ld/st below need the whole warp converged
-        if constexpr (OPT) {
-          if (a.cap_log2 > 0.f) {
-#pragma unroll
-            for (int c = 0; c < C; ++c)
-              sr[c] = __float_as_uint(capped_score(__uint_as_float(sr[c]) * a.cap_arg, a.cap_log2));
-          }
-        }
         const int32_t lo = OPT ? pos - a.window + 1 : 0;  // first key the row sees
         if (__all_sync(0xffffffffu, k0 + C - 1 <= pos && (!OPT || k0 >= lo))) {
 #pragma unroll
@@ -570,31 +566,40 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
           for (int c = 0; c < C; ++c)
             x[c] = k0 + c <= pos && (!OPT || k0 + c >= lo) ? __uint_as_float(sr[c]) : -INFINITY;
         }
-#pragma unroll
-        for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
-        float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-        mx *= sl2;  // scale > 0 keeps the order
         float alpha = 1.f;
         bool resc = false;
-        if (mx > m_ref + 8.f) {
-          alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
-          l *= alpha;
-          resc = j > 0 && (!OPT || m_ref != -INFINITY);  // (O is 0 while m_ref is -inf)
-          m_ref = mx;
-        }
         uint32_t ph[C / 2];
-        // weights as packed pairs: (x0, x1) * scale - m in one instruction, the
-        // sums in two packed partial sums (short dependence chains)
-        const float2 sc2 = make_float2(sl2, sl2), nm2 = OPT && m_ref == -INFINITY ? make_float2(0.f, 0.f) : make_float2(-m_ref, -m_ref);
-        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        if constexpr (OPT) {
+          row_weights(a, x, amax, poly, m_ref, l, alpha, resc, ph);
+        } else {
+          // the row maximum over 4 independent partial maxima (three-input max:
+          // short dependence chains, one instruction per two scores)
+          float pm[4];
 #pragma unroll
-        for (int c = 0; c < C / 2; ++c) {
-          const float2 y = ffma2(make_float2(x[2 * c], x[2 * c + 1]), sc2, nm2);
-          const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-          part[c & 1] = fadd2(part[c & 1], pp);
-          ph[c] = pack_f16(pp.x, pp.y);  // weights <= 2^8
+          for (int u = 0; u < 4; ++u) pm[u] = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
+          float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+          mx *= sl2;  // scale > 0 keeps the order
+          if (mx > m_ref + 8.f) {
+            alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
+            l *= alpha;
+            resc = j > 0;
+            m_ref = mx;
+          }
+          // weights as packed pairs: (x0, x1) * scale - m in one instruction, the
+          // sums in two packed partial sums (short dependence chains)
+          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_ref, -m_ref);
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+          for (int c = 0; c < C / 2; ++c) {
+            const float2 y = ffma2(make_float2(x[2 * c], x[2 * c + 1]), sc2, nm2);
+            const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+            part[c & 1] = fadd2(part[c & 1], pp);
+            ph[c] = pack_f16(pp.x, pp.y);  // weights <= 2^8
+          }
+          l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
         }
-        l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
         __syncwarp();
         tc::st32(trow + D + sb * C, ph);
         if (__any_sync(0xffffffffu, resc)) {
@@ -635,7 +640,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         float inv;
         if constexpr (OPT) {
           float lse;
-          inv = finish_row(a.sinks, g * G + h, m_ref, l, lse) * (F8 ? a.v_scale : 1.f);
+          inv = finish_row(a.sinks, g * GG + h, m_ref, l, lse) * (F8 ? a.v_scale : 1.f);
           if (valid && a.lse) a.lse[orow] = lse;
         } else {
           inv = (F8 ? a.v_scale : 1.f) / l;
@@ -671,9 +676,9 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
             for (int i = 0; i < 8; ++i) {
               const int rw = 4 * i + (lane >> 3);
               const int rr = (warp & 3) * 32 + rw;
-              const int32_t tk = tok0 + rr / G;
+              const int32_t tk = tok0 + tok_of(rr);
               if (tk < n) {
-                const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * G + rr % G;
+                const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * GG + head_of(rr);
                 *reinterpret_cast<uint4*>(a.out16 + orr * D + q * 64 + pc * 8) =
                     *reinterpret_cast<const uint4*>(stg + rw * 128 + ((pc ^ (rw & 7)) << 4));
               }
@@ -706,7 +711,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
             if (warp_wait(&o_staged, 0, &ps.abort_flag) && lane == 0) {
 #pragma unroll
               for (int q = 0; q < D / 32; ++q)
-                tma_store_3d(&tmo, smem_u32(stg) + q * (128 * 128), q * 32, g * G, q0 + tok0);
+                tma_store_3d(&tmo, smem_u32(stg) + q * (128 * 128), q * 32, g * GG, q0 + tok0);
               bulk_commit();
               bulk_wait_read();
             }
@@ -737,9 +742,9 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
           for (int i = 0; i < 8; ++i) {
             const int rw = 4 * i + (lane >> 3);         // row within the warp's 32
             const int rr = (warp & 3) * 32 + rw;        // row within the tile
-            const int32_t tk = tok0 + rr / G;
+            const int32_t tk = tok0 + tok_of(rr);
             if (tk < n) {
-              const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * G + rr % G;
+              const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * GG + head_of(rr);
               *reinterpret_cast<float4*>(a.out + orr * D + q * 32 + pc * 4) =
                   *reinterpret_cast<const float4*>(stg + rw * 128 + ((pc ^ (rw & 7)) << 4));
             }

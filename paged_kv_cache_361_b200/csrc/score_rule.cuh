@@ -14,6 +14,111 @@ __device__ __forceinline__ float capped_score(float z, float cap_log2) {
   return fmaf(-2.f * cap_log2, __fdividef(1.f, fast_exp2(z) + 1.f), cap_log2);
 }
 
+// The same without exponentials for small y: tanh(y) = y P(y^2), P(z) = 1 + z Q(z),
+// Q of degree 1 or 3 fitted by least squares in Chebyshev polynomials at 400
+// Chebyshev nodes of z. With the fp32 coefficients y P is within 9e-8 of tanh(y)
+// up to 0.2 (degree 1) and within 3e-8 up to 0.5: 6e-6 and 2e-6 for a cap of 50
+// in base 2. Four or six multiply-adds a score, where the exponentials are three
+// operations of a pipe that does one for every eight multiply-adds.
+constexpr float kCapSmall = 0.2f, kCapMedium = 0.5f;
+
+// P scaled by cap_log2: the capped score of y in base 2 is y times the value at
+// y^2 (y = -inf gives +inf: a masked score stays -inf).
+__device__ __forceinline__ float2 cap_poly(const float2 z, const float c0, const float c1, const float c2) {
+  return ffma2(ffma2(make_float2(c2, c2), z, make_float2(c1, c1)), z, make_float2(c0, c0));
+}
+struct CapPoly {
+  float one, s[2], m[4];
+  __device__ __forceinline__ explicit CapPoly(float cap_log2) {
+    one = cap_log2;
+    s[0] = -0.333322763f * cap_log2;
+    s[1] = 0.131206915f * cap_log2;
+    m[0] = -0.333333105f * cap_log2;
+    m[1] = 0.133305132f * cap_log2;
+    m[2] = -0.0533910543f * cap_log2;
+    m[3] = 0.0179992188f * cap_log2;
+  }
+  __device__ __forceinline__ float2 small(float2 y) const { return cap_poly(fmul2(y, y), one, s[0], s[1]); }
+  __device__ __forceinline__ float2 medium(float2 y) const {
+    const float2 z = fmul2(y, y), q = cap_poly(z, m[1], m[2], m[3]);
+    return ffma2(ffma2(q, z, make_float2(m[0], m[0])), z, make_float2(one, one));
+  }
+};
+
+// The weights of a softmax thread's 64 scores x (one row, raw, masked ones
+// -inf), for both tcgen05 kernels: moves the running maximum m (base 2) when a
+// score exceeds it by 8, scaling l by alpha and saying whether O has to be
+// scaled too; adds the weights to l and packs them as f16 (they are at most 2^8).
+//   amax: largest |score| of the row, masked ones included (capped scores)
+template <int C, class Args>
+__device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], float amax, const CapPoly& poly,
+                                            float& m, float& l, float& alpha, bool& rescale, uint32_t (&ph)[C / 2]) {
+  float pm[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u) pm[u] = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
+  float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+  const bool capped = a.cap_log2 > 0.f;
+  if (!capped)
+    mx *= a.scale_log2;  // scale > 0 keeps the order
+  else if (mx != -INFINITY)
+    mx = capped_score(mx * a.cap_arg, a.cap_log2);
+  alpha = 1.f;
+  rescale = false;
+  if (mx > m + 8.f) {
+    alpha = fast_exp2(m - mx);  // 0 while m is -inf
+    l *= alpha;
+    rescale = m != -INFINITY;   // (O is 0 while m is -inf)
+    m = mx;
+  }
+  const float nm = m == -INFINITY ? 0.f : -m;  // a row that has seen nothing: weights 0
+  const float2 nm2 = make_float2(nm, nm);
+  float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+  auto weigh = [&](auto score) {
+#pragma unroll
+    for (int c = 0; c < C / 2; ++c) {
+      const float2 y = score(make_float2(x[2 * c], x[2 * c + 1]));
+      const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+      part[c & 1] = fadd2(part[c & 1], pp);
+      const __half2 h = __floats2half2_rn(pp.x, pp.y);
+      ph[c] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+  };
+  if (!capped) {
+    const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
+    weigh([&](float2 s) { return ffma2(s, sc2, nm2); });
+  } else if (__all_sync(0xffffffffu, amax * a.cap_k <= kCapSmall)) {
+    const float2 k2 = make_float2(a.cap_k, a.cap_k);
+    weigh([&](float2 s) {
+      const float2 y = fmul2(s, k2);
+      return ffma2(y, poly.small(y), nm2);
+    });
+  } else if (__all_sync(0xffffffffu, amax * a.cap_k <= kCapMedium)) {
+    const float2 k2 = make_float2(a.cap_k, a.cap_k);
+    weigh([&](float2 s) {
+      const float2 y = fmul2(s, k2);
+      return ffma2(y, poly.medium(y), nm2);
+    });
+  } else {
+    weigh([&](float2 s) {
+      return make_float2(s.x == -INFINITY ? -INFINITY : capped_score(s.x * a.cap_arg, a.cap_log2) + nm,
+                         s.y == -INFINITY ? -INFINITY : capped_score(s.y * a.cap_arg, a.cap_log2) + nm);
+    });
+  }
+  l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+}
+
+// Largest |x| of raw scores.
+template <int C>
+__device__ __forceinline__ float row_amax(const uint32_t (&s)[C]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c)
+    m[c & 3] = fmax3(m[c & 3], fabsf(__uint_as_float(s[2 * c])), fabsf(__uint_as_float(s[2 * c + 1])));
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+
 // The end of a row of head h: (m, l) of all its keys in base 2 with the head's
 // sink, as the factor of o and the log-sum-exp. A row that sees nothing gives
 // 0 and its sink, or -inf.

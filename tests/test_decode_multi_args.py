@@ -33,8 +33,8 @@ def test_invalid_arguments(kw):
 
 @pytest.mark.parametrize("kw,cache", [
     (dict(mq=17), {}), (dict(hq=6), {}), (dict(hq=32), {}), ({}, dict(block_size=4)), ({}, dict(dtype=B.PA_F32)),
-    ({}, dict(head_dim=256)), ({}, dict(num_blocks=2 ** 28)), (dict(n=65536), {}),
-    (dict(mc=2 ** 30 + 1, mb=2 ** 27), {}), (dict(mc=2 ** 23, mb=2 ** 20, P=64), {})])
+    ({}, dict(head_dim=256)), ({}, dict(num_blocks=2 ** 28)), (dict(mc=2 ** 30 + 1, mb=2 ** 27), {}),
+    (dict(n=2 ** 30, T=2 ** 30, P=0), {})])
 def test_unsupported(kw, cache):
     assert _call(cache, **kw) == B.PA_ERR_UNSUPPORTED
 
@@ -45,13 +45,15 @@ def test_empty_calls():
 
 
 def test_workspace_bytes():
+    """Two partials a worker, (m, l) and o, of the rows of a (sequence, kv head)."""
     f = B.pa_decode_multi_workspace_bytes
-    row = lambda T, hq, parts, D: -(-T * hq * parts * 8 // 256) * 256 + T * hq * parts * D * 4
-    assert f(4, 4, 1, 32, 8, 128, 4096, 0, 0) == 0                       # not split
-    assert f(4, 4, 1, 32, 8, 128, 4096, 0, 1024) == row(4, 32, 5, 128)   # 4096 + 63 keys in 1024s
-    assert f(4, 4, 1, 32, 8, 128, 4096, 1000, 512) == row(4, 32, 3, 128)  # 1000 + 63
-    assert f(8, 4, 2, 32, 8, 128, 4096, 1000, 512) == row(8, 32, 3, 128)  # 1001 + 63
-    assert f(4, 4, 1, 32, 8, 128, 100, 0, 512) == 0                      # fits one partition
+    need = lambda workers, rows, D: -(-2 * workers * rows * 8 // 256) * 256 + 2 * workers * rows * D * 4
+    assert f(4, 4, 1, 32, 8, 128, 4096, 0, 0) == 0                        # not split
+    assert f(4, 4, 1, 32, 8, 128, 1, 0) == 0                              # one chunk a sequence
+    assert f(4, 4, 1, 32, 8, 128, 4096, 0) == need(444, 4, 128)           # 3 CTAs per SM
+    assert f(20, 4, 5, 32, 8, 128, 4096, 0) == need(148, 20, 128)         # on tcgen05: one
+    assert f(4, 4, 1, 32, 8, 64, 65, 0) == need(4 * 8 * 2, 4, 64)         # fewer chunks than workers: 65 + 63 keys
+    assert f(4, 4, 1, 32, 8, 128, 4096, 1000, 512) == need(4 * 8 * 9 // 4, 4, 128)   # 1000 + 63 keys in 128s, 4 a share
     for bad in ((0, 4, 1, 32, 8, 128, 4096), (4, 4, 17, 32, 8, 128, 4096), (4, 4, 1, 30, 8, 128, 4096),
                 (4, 4, 1, 32, 8, 128, -1), (4, 4, 1, 32, 8, 128, 2 ** 30 + 1)):
         assert f(*bad) == 0

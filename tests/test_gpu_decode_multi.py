@@ -4,13 +4,13 @@ Bounds, for |q|, |k|, |v| of N(0, 1) and scale D^-1/2. A score is a sum of D
 products in fp32, off by at most D 2^-24 sum|q_i k_i| scale < 1e-4 (D 128: the
 sum is near 82, the scale 0.088); a capped one by a few 2^-24 of twice the cap
 in base 2 more (cap 50: 2e-5). So a weight over the denominator is off by 2e-4
-of itself at most, and by its rounding: with up to 16 rows (new tokens x query
+of itself at most, and by its rounding: with up to 8 rows (new tokens x query
 heads of a kv head) over a bf16 cache it is split in two bf16 (2^-16), otherwise
 rounded to f16 (half a step, 2^-11). With size = sum_j w_j |v_j| / den, the
 result before its rounding to bf16 (half a step, 2^-8 of itself) is off by at
 most W size, W = 2^-12 where it is split, else 2^-11 + 2^-12: for a weight
 w' = w (1 + e), |e| <= 2^-11, |sum w'_j v_j - sum w_j v_j| / den <= 2^-11 size,
-and the denominator sums the weights before that rounding. With more than 16
+and the denominator sums the weights before that rounding. With more than 8
 rows V too is f16: exact from 2^-14 up, off by 2^-25 at most below, which a
 weighted mean does not enlarge (2^-24 for the bound, over bf16).
 The log-sum-exp is off by the score's error, at most 1.2e-4 with the base
@@ -104,7 +104,7 @@ class Batch:
 
     def check(self, counts, q, out, lse, window=0, cap=0.0, sinks=None):
         hq, hkv = q.shape[1], self.kc.shape[1]
-        f16 = self.dtype != "bf16" or max(counts) * (hq // hkv) > 16
+        f16 = self.dtype != "bf16" or max(counts) * (hq // hkv) > 8
         at = 0
         for i, n in enumerate(counts):
             ref, want, size = options_attention(q[at:at + n], self.rows[0][i], self.rows[1][i], q.shape[2] ** -0.5,
@@ -184,6 +184,33 @@ def test_empty_contexts_and_one_row_per_sequence():
     b = Batch([0, 0], 2, 64, 8, "bf16")
     q, out, lse = b.run([1, 1], 4, cu=False)
     assert not out.any() and (lse == float("-inf")).all()
+
+
+def test_many_empty_and_short_sequences_between_long_ones():
+    """Runs of sequences without rows, without keys (more tokens than context is an
+    error; so is none) and of one key, between ones that several CTAs share."""
+    lens = [0, 3000, 1, 1, 0, 0, 1, 0, 2500, 1, 1, 1, 64, 0, 1, 700, 0]
+    for G in (1, 2, 8):
+        b = Batch(lens, 2, 64, 16, "bf16", seed=G)
+        for P in (-1, 0, 64, 448):
+            counts = [1] * len(lens)
+            b.check(counts, *b.run(counts, 2 * G, 0, 0.0, _sinks(2 * G), P, cu=False), 0, 0.0, _sinks(2 * G))
+            counts = [min(x, (i * 5) % 7) for i, x in enumerate(lens)]
+            b.check(counts, *b.run(counts, 2 * G, 900, 0.0, None, P), 900)
+    assert B.pa_get_device_error()[0] == B.PA_OK
+
+
+def test_even_shares_over_a_large_ragged_batch():
+    """300 sequences from 1 to 1900 tokens, so that every CTA has several segments."""
+    g = torch.Generator().manual_seed(77)
+    lens = torch.randint(1, 1900, (300,), generator=g).tolist()
+    counts = [min(x, int(n)) for x, n in zip(lens, torch.randint(0, 5, (300,), generator=g))]
+    for dtype, G in (("bf16", 2), ("int8", 1), ("bf16", 8), ("e4m3", 4)):
+        b = Batch(lens, 1, 64, 16, dtype, seed=G)
+        for window in (0, 300):
+            b.check(counts, *b.run(counts, G, window), window)
+            b.check([1] * 300, *b.run([1] * 300, G, window, cu=False), window)
+    assert B.pa_get_device_error()[0] == B.PA_OK
 
 
 def test_partitions_agree_and_long_context():
@@ -307,7 +334,7 @@ def test_wrong_tensors_are_refused():
     cu = torch.tensor([0, 2, 4], dtype=torch.int32).cuda()
     args = dict(q=q, cu_q_lens=cu, k_cache=b.kc, v_cache=b.vc, block_tables=b.tables.cuda(),
                 context_lens=torch.tensor([50, 60], dtype=torch.int32).cuda(), scale=0.125, out=torch.empty_like(q),
-                max_q_len=2, max_context_len=60)
+                max_q_len=2, max_context_len=60, partition_tokens=0)
     B.pa_decode_multi(**args)
     for kw in (dict(q=q.float()), dict(out=torch.empty(4, 4, 64, device="cuda")), dict(cu_q_lens=cu[:2]),
                dict(cu_q_lens=cu.long()), dict(block_tables=b.tables.cuda()[:1]), dict(context_lens=args["context_lens"].cpu()),

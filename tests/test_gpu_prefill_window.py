@@ -118,6 +118,17 @@ def test_sinks_of_every_size_and_growing_scores():
         _check(b, [300], q, out.cpu(), lse.cpu(), window, cap)
 
 
+@pytest.mark.parametrize("cap", [0.01, 1.5, 5.0, 6.5, 1000.0])
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+def test_caps_of_every_size(cap, dtype):
+    """From caps that flatten every score, past those where rows are on both
+    sides of the polynomial's range, to one that changes nothing much."""
+    b = Batch([200, 90], 2, 128, 16, dtype, seed=8)
+    _check(b, [200, 40], *_run(b, [200, 40], 8, 0, cap), 0, cap)
+    b.check([5, 16], *b.run([5, 16], 8, 70, cap), 70, cap)
+    b.check([1, 2], *b.run([1, 2], 8, 70, cap), 70, cap)
+
+
 def test_rows_of_no_sequence_stay_and_bad_rows_are_left_out():
     b = Batch([150, 60], 2, 64, 16, "bf16")
     q = torch.randn(200, 4, 64).bfloat16().cuda()
