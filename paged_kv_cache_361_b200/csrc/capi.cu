@@ -952,6 +952,7 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.bs = cache->block_size;
   a.max_blocks = max_blocks_per_seq;
   a.max_ctx = max_context_len;
+  a.bshift = cache->block_size == 8 ? 3 : (cache->block_size == 16 ? 4 : 5);
   a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
   a.window = window > 0 && window < max_context_len ? window : (max_context_len > 0 ? max_context_len : 1);
   a.per = plan.per;

@@ -43,6 +43,7 @@ struct MultiArgs {
   int64_t num_blocks;
   int32_t num_seqs, num_tokens, max_q, hq, hkv, bs, max_blocks, max_ctx;
   int32_t gshift;          // log2 of hq / hkv
+  int32_t bshift;          // log2 of block_size
   int32_t window;          // >= 1; max_ctx or more: every earlier key
   int32_t per;             // chunks of a worker; 0: even shares, kWholeUnits: a unit each
   int32_t slot_rows;       // rows of a partial: max_q hq / hkv
@@ -192,6 +193,37 @@ struct MultiWalk {
   }
 };
 
+// A producer warp's block ids: lane i holds that of the chunk's block i, read
+// from the table one chunk ahead. (A window of ids shared by shuffles, and block
+// numbers by division, took the producer 2000 cycles a chunk, which set the
+// kernel's pace.)
+template <int KEYS>
+struct BlocksAhead {
+  const int32_t* row;
+  int32_t end, nxt;  // blocks of the segment end before `end`
+  __device__ __forceinline__ int32_t fetch(const MultiArgs& a, int32_t key, int lane) const {
+    const int32_t i = (key >> a.bshift) + lane;
+    return lane < (KEYS >> a.bshift) && i < end ? __ldg(row + i) : -1;
+  }
+  __device__ __forceinline__ void init(const MultiArgs& a, const MultiSegment& e, int lane) {
+    row = a.tables + static_cast<int64_t>(e.s) * a.max_blocks;
+    end = min(a.max_blocks, (e.kend + a.bs - 1) >> a.bshift);
+    nxt = fetch(a, e.begin, lane);
+  }
+  // Block of this lane in the chunk at `key`; true if it holds a key in [kbeg,
+  // kend) and its id is in the pool (if not, that is recorded).
+  __device__ __forceinline__ bool next(const MultiArgs& a, const MultiSegment& e, int32_t key, int lane, bool report,
+                                       int32_t& blk) {
+    blk = nxt;
+    nxt = fetch(a, key + KEYS, lane);
+    if (lane >= (KEYS >> a.bshift) || (key >> a.bshift) + lane >= end || key + ((lane + 1) << a.bshift) <= e.kbeg)
+      return false;
+    const bool ok = blk >= 0 && blk < a.num_blocks;
+    if (!ok && report) record_error(PA_ERR_DEVICE_BOUNDS, blk);
+    return ok;
+  }
+};
+
 // Row of q, out and lse of row rho of a segment.
 __device__ __forceinline__ int64_t multi_row(const MultiArgs& a, const MultiSegment& e, int rho) {
   return static_cast<int64_t>(e.ms.q0 + (rho >> a.gshift)) * a.hq + (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1));
@@ -269,9 +301,8 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
     const uint64_t pol = kv_stream_policy();
     int jg = 0;
     while (walk.next(a, e)) {
-      TableAhead ta;
-      ta.init(a.tables + static_cast<int64_t>(e.s) * a.max_blocks, e.begin / a.bs,
-              min(a.max_blocks, (e.kend + a.bs - 1) / a.bs), lane);
+      BlocksAhead<C> ahead;
+      ahead.init(a, e, lane);
       bool gave_up = false;
       for (int j = 0; j < e.chunks; ++j, ++jg) {
         const int st = jg % S;
@@ -279,36 +310,22 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
           gave_up = true;
           break;
         }
-        bool ok[MT];
-        int32_t blk[MT];
-        int cnt = 0;
-#pragma unroll
-        for (int u = 0; u < MT; ++u) {  // 64 keys at a time: at most 8 blocks (bs >= 8)
-          const int32_t h0 = e.begin + j * C + u * 64;
-          const int32_t nb = h0 < e.kend ? (min(64, e.kend - h0) + a.bs - 1) / a.bs : 0;
-          blk[u] = ta.get(h0 / a.bs, nb, lane);
-          ok[u] = false;
-          if (lane < nb && h0 + (lane + 1) * a.bs > e.kbeg) {
-            ok[u] = blk[u] >= 0 && blk[u] < a.num_blocks;
-            if (!ok[u]) record_error(PA_ERR_DEVICE_BOUNDS, blk[u]);
-          }
-          cnt += __popc(__ballot_sync(0xffffffffu, ok[u]));
-        }
+        int32_t blk;
+        const bool ok = ahead.next(a, e, e.begin + j * C, lane, true, blk);
+        const int cnt = __popc(__ballot_sync(0xffffffffu, ok));
         if (lane == 0) mbar_arrive_expect_tx(&ps.full[st], 2u * cnt * box_bytes);
         __syncwarp();
-#pragma unroll
-        for (int u = 0; u < MT; ++u)
-          if (ok[u]) {
-            const int32_t y = (blk[u] * a.hkv + e.g) * a.bs;
-            const uint32_t kdst = sbase + st * Cfg::kStageBytes + u * (64 * D * Cfg::kEl) + lane * box_bytes;
-            if constexpr (CF != 0) {
-              tma_load_2d(kdst, &tmk, 0, y, &ps.full[st], pol);
-              tma_load_2d(kdst + Cfg::kTileBytes, &tmv, 0, y, &ps.full[st], pol);
-            } else {
-              tma_block<D>(kdst, &tmk, y, &ps.full[st], pol);
-              tma_block<D>(kdst + Cfg::kTileBytes, &tmv, y, &ps.full[st], pol);
-            }
+        if (ok) {
+          const int32_t y = (blk * a.hkv + e.g) * a.bs;
+          const uint32_t kdst = sbase + st * Cfg::kStageBytes + lane * box_bytes;
+          if constexpr (CF != 0) {
+            tma_load_2d(kdst, &tmk, 0, y, &ps.full[st], pol);
+            tma_load_2d(kdst + Cfg::kTileBytes, &tmv, 0, y, &ps.full[st], pol);
+          } else {
+            tma_block<D>(kdst, &tmk, y, &ps.full[st], pol);
+            tma_block<D>(kdst + Cfg::kTileBytes, &tmv, y, &ps.full[st], pol);
           }
+        }
       }
       if (gave_up) break;
     }

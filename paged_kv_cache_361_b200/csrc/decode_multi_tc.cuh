@@ -48,7 +48,9 @@ struct MultiTcCfg {
   static constexpr int kSmemBytes = 1024 + kQBytes + kStages * kStageBytes + kCodeStages * kCodeStageBytes;
   static constexpr int kProducerWarp = 8, kMmaWarp = 9, kConvWarp0 = 10, kConvWarps = 4, kVProducerWarp = 14;
   static constexpr int kThreads = 32 * (F8 ? 14 : 15);
-  static constexpr uint32_t kTileCols = D + 2 * kHalf;      // TMEM of a half: O, then two S/P buffers
+  // TMEM: O of each half, then two buffers of S (keys of half 0, then 1), each
+  // half's P in the place of its S
+  static constexpr uint32_t kSCol = 2 * D;
   static constexpr int kRowPitch = D + 4;                   // floats of a row in the fold
   static constexpr int kMinChunks = 4;                      // of a share
   static_assert(kSmemBytes <= 226 * 1024, "shared memory");
@@ -68,7 +70,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
   __shared__ uint64_t kfull[S], kempty[S];             // 16-bit stages (bf16: their K)
   __shared__ uint64_t vfull[S], vempty[S], vready[S];  // bf16: V of a stage, and V rewritten as f16
   __shared__ uint64_t cfull[CS], cempty[CS];           // 8-bit: code staging ring
-  __shared__ uint64_t s_full[2][2], p_full[2][2], o_bar[2], o_last[2], q_full, drain;
+  __shared__ uint64_t s_full[2], p_full[2][2], o_bar[2], o_last[2], q_full, drain;
   __shared__ uint64_t seg_done;  // a segment's rows are out: its stages (the fold's memory) may be filled again
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag, stop;
@@ -87,8 +89,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
     mbar_init(&drain, 1);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&s_full[t][0], 1);
-      mbar_init(&s_full[t][1], 1);
+      mbar_init(&s_full[t], 1);
       mbar_init(&p_full[t][0], 4);
       mbar_init(&p_full[t][1], 4);
       mbar_init(&o_bar[t], 1);
@@ -136,9 +137,8 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
     int si = 0;  // segments with keys so far
     while (ok && walk.next(a, e)) {
       if (e.chunks == 0) continue;
-      TableAhead ta;
-      ta.init(a.tables + static_cast<int64_t>(e.s) * a.max_blocks, e.begin / a.bs,
-              min(a.max_blocks, (e.kend + a.bs - 1) / a.bs), lane);
+      BlocksAhead<CK> ahead;
+      ahead.init(a, e, lane);
       if (si > 0 && !warp_wait(&seg_done, (si - 1) & 1, &abort_flag)) break;
       ++si;
       for (int j = 0; j < e.chunks; ++j, ++jg) {
@@ -147,37 +147,24 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
           ok = false;
           break;
         }
-        bool in[2] = {false, false};
-        int32_t blk[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {  // 64 keys at a time: at most 8 blocks each
-          const int32_t h0 = e.begin + j * CK + u * C;
-          const int32_t nb = h0 < e.kend ? (min(C, e.kend - h0) + a.bs - 1) / a.bs : 0;
-          blk[u] = ta.get(h0 / a.bs, nb, lane);
-          if (lane < nb && h0 + (lane + 1) * a.bs > e.kbeg) {
-            in[u] = blk[u] >= 0 && blk[u] < a.num_blocks;
-            if (!in[u] && !is_v) record_error(PA_ERR_DEVICE_BOUNDS, blk[u]);
-          }
-        }
-        const int cnt = __popc(__ballot_sync(0xffffffffu, in[0])) + __popc(__ballot_sync(0xffffffffu, in[1]));
+        int32_t blk;
+        const bool in = ahead.next(a, e, e.begin + j * CK, lane, !is_v, blk);
+        const int cnt = __popc(__ballot_sync(0xffffffffu, in));
         if (lane == 0) mbar_arrive_expect_tx(&full[st], (F8 ? 2u : Cfg::kCols) * cnt * box_bytes);
         __syncwarp();
+        if (in) {
+          const int32_t y = (blk * a.hkv + e.g) * a.bs;
+          if constexpr (F8) {
+            const uint32_t dst = cs0 + st * Cfg::kCodeStageBytes + lane * box_bytes;
+            tma_load_2d(dst, &tmk, 0, y, &full[st], pol);
+            tma_load_2d(dst + Cfg::kCodeTileBytes, &tmv, 0, y, &full[st], pol);
+          } else {
+            const uint32_t dst = kv0 + st * Cfg::kStageBytes + (is_v ? Cfg::kTileBytes : 0) + lane * box_bytes;
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-          if (in[u]) {
-            const int32_t y = (blk[u] * a.hkv + e.g) * a.bs;
-            const uint32_t off = u * (C * (F8 ? D : 128)) + lane * box_bytes;
-            if constexpr (F8) {
-              const uint32_t dst = cs0 + st * Cfg::kCodeStageBytes + off;
-              tma_load_2d(dst, &tmk, 0, y, &full[st], pol);
-              tma_load_2d(dst + Cfg::kCodeTileBytes, &tmv, 0, y, &full[st], pol);
-            } else {
-              const uint32_t dst = kv0 + st * Cfg::kStageBytes + (is_v ? Cfg::kTileBytes : 0) + off;
-#pragma unroll
-              for (int hf = 0; hf < Cfg::kCols; ++hf)
-                tma_load_2d(dst + hf * Cfg::kColBytes, map, hf * 64, y, &full[st], pol);
-            }
+            for (int hf = 0; hf < Cfg::kCols; ++hf)
+              tma_load_2d(dst + hf * Cfg::kColBytes, map, hf * 64, y, &full[st], pol);
           }
+        }
       }
     }
     if (abort_flag && lane == 0)  // copies already started land before exit
@@ -227,29 +214,31 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
       }
     }
   } else if (warp == Cfg::kMmaWarp) {
-    // ---- MMA issuer: S_t(j + 1) of both halves, then O_t += P_t(j) V_t(j) ----
-    constexpr uint32_t kIdS = F8 ? tc::idesc_f16(128, C, false) : tc::idesc_bf16(128, C, false);
+    // ---- MMA issuer: S(j + 1), then O_t += P_t(j) V_t(j) of each half. S is one
+    // product over the stage's 128 keys (64 cycles a step; two of 64 keys, bound by
+    // reading q twice, 96) ----
+    constexpr uint32_t kIdS = F8 ? tc::idesc_f16(128, CK, false) : tc::idesc_bf16(128, CK, false);
     constexpr uint32_t kIdPV = tc::idesc_f16(128, D, true);
     const uint64_t qdesc0 = tc::smem_desc(sbase, 16, 1024);
     const uint64_t kdesc0 = tc::smem_desc(kv0, 16, 1024);
     const uint64_t vdesc0 = tc::smem_desc(kv0 + Cfg::kTileBytes, Cfg::kCols > 1 ? Cfg::kColBytes : 1024, 1024);
-    auto issue_s = [&](int t, int j) {
-      const uint64_t kb = kdesc0 + static_cast<uint64_t>(((j % S) * Cfg::kStageBytes + t * C * 128) >> 4);
-      const uint32_t dst = tmem + t * Cfg::kTileCols + D + (j & 1) * C;
+    auto issue_s = [&](int j) {
+      const uint64_t kb = kdesc0 + static_cast<uint64_t>(((j % S) * Cfg::kStageBytes) >> 4);
+      const uint32_t dst = tmem + Cfg::kSCol + (j & 1) * CK;
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
         const uint32_t offq = static_cast<uint32_t>((kk >> 2) * Cfg::kQColBytes + (kk & 3) * 32) >> 4;
         const uint32_t offk = static_cast<uint32_t>((kk >> 2) * Cfg::kColBytes + (kk & 3) * 32) >> 4;
         tc::mma_ss(dst, qdesc0 + offq, kb + offk, kIdS, kk > 0);
       }
-      tc::commit(smem_u32(&s_full[t][j & 1]));
+      tc::commit(smem_u32(&s_full[j & 1]));
     };
     auto issue_pv = [&](int t, int j, bool first, bool last) -> bool {
       const int sb = j & 1;
       if (!warp_wait(&p_full[t][sb], (j >> 1) & 1, &abort_flag)) return false;
       tc::fence_after();
       const uint64_t vb = vdesc0 + static_cast<uint64_t>(((j % S) * Cfg::kStageBytes + t * C * 128) >> 4);
-      const uint32_t to = tmem + t * Cfg::kTileCols, tp = to + D + sb * C;
+      const uint32_t to = tmem + t * D, tp = tmem + Cfg::kSCol + sb * CK + t * C;
 #pragma unroll
       for (int ks = 0; ks < C / 16; ++ks)
         tc::mma_ts(to, tp + ks * 8, vb + static_cast<uint64_t>((ks * 16 * 128) >> 4), kIdPV, !first || ks > 0);
@@ -268,16 +257,14 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
       ++qi;
       tc::fence_after();
       if (ok) {
-        issue_s(0, j0);
-        issue_s(1, j0);
+        issue_s(j0);
         if constexpr (!F8) tc::commit(smem_u32(&kempty[j0 % S]));  // the stage's K is read once these finish
       }
       for (int j = j0; ok && j < j1; ++j) {
         if (j + 1 < j1) {
           if (!(ok = warp_wait(&kfull[(j + 1) % S], ((j + 1) / S) & 1, &abort_flag))) break;
           tc::fence_after();
-          issue_s(0, j + 1);
-          issue_s(1, j + 1);
+          issue_s(j + 1);
           if constexpr (!F8) tc::commit(smem_u32(&kempty[(j + 1) % S]));
         }
         if constexpr (!F8) {
@@ -296,7 +283,8 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
   } else if (warp < 8) {
     // ---- softmax of half t: thread = row rho of replica rep ----
     const int t = warp >> 2, r = tid & 127, rho = r % RC, rep = r / RC;
-    const uint32_t trow = tmem + t * Cfg::kTileCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    const uint32_t trow = lanes + t * D, srow = lanes + Cfg::kSCol + t * C;  // O, and S of buffer 0
     float* stage0 = reinterpret_cast<float*>(sgen + Cfg::kQBytes);  // the fold: rows of O, then (m, l) of each half
     float* stg = stage0 + r * Cfg::kRowPitch;
     float* ml = stage0 + 128 * Cfg::kRowPitch;
@@ -338,7 +326,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
       }
       for (int j = 0; j < e.chunks; ++j, ++jg) {
         const int sb = jg & 1;
-        if (!warp_wait(&s_full[t][sb], (jg >> 1) & 1, &abort_flag)) {
+        if (!warp_wait(&s_full[sb], (jg >> 1) & 1, &abort_flag)) {
           ok = false;
           break;
         }
@@ -346,10 +334,10 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
           tc::fence_after();
           uint32_t sr[CW];
           if constexpr (RF == 4) {
-            tc::ld16(trow + D + sb * C + rep * CW, sr);
+            tc::ld16(srow + sb * CK + rep * CW, sr);
           } else {
-            tc::ld32(trow + D + sb * C + rep * CW, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-            if constexpr (RF == 1) tc::ld32(trow + D + sb * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+            tc::ld32(srow + sb * CK + rep * CW, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+            if constexpr (RF == 1) tc::ld32(srow + sb * CK + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
           }
           tc::wait_ld();
           const int32_t k0 = e.begin + j * CK + t * C + rep * CW;
@@ -369,7 +357,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < C / 2; ++c) pw[c] = RF == 1 || c / (CW / 2) == rep ? ph[c % (CW / 2)] : 0u;
           __syncwarp();
-          tc::st32(trow + D + sb * C, pw);
+          tc::st32(srow + sb * CK, pw);
           if (__any_sync(0xffffffffu, resc)) {
             // O must hold P(j-1) V(j-1) before it is rescaled
             if (!warp_wait(&o_bar[t], (jg - 1) & 1, &abort_flag)) {
