@@ -17,6 +17,7 @@
 #include "decode_simt.cuh"
 #include "prefill_mma.cuh"
 #include "prefill_tc.cuh"
+#include "prefill_window.cuh"
 #include "rotary.cuh"
 
 namespace {
@@ -463,15 +464,13 @@ pa_status launch_multi(const MultiArgs& a, const MultiPlan& p, const CUtensorMap
   return launch_kernel(merge, grid, dim3(32 * kMultiMergeWarps), 0, st, true, a);
 }
 
-// pa_prefill_window: the prefill kernel with the score rule.
 template <int D, int CF>
-pa_status launch_prefill_window(const PrefillArgs& a, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
+pa_status launch_prefill_window(const WindowArgs& a, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tq, cudaStream_t st) {
-  constexpr int TILES = 2;
-  using Cfg = TcCfg<D, TILES, CF != 0>;
-  auto kern = prefill_tc_kernel<D, 0, TILES, CF, true>;
+  using Cfg = WindowCfg<D, CF>;
+  auto kern = a.cap_log2 > 0.f ? prefill_window_kernel<D, CF, true> : prefill_window_kernel<D, CF, false>;
   if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, false)) return PA_ERR_CUDA;
-  kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, tq, tq, a);  // (no output map: O goes out through plain stores)
+  kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, tq, a);
   return launched();
 }
 
@@ -833,45 +832,43 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
       (reinterpret_cast<uintptr_t>(context_lens) & 3))
     return PA_ERR_INVALID_ARG;
   const int D = cache->head_dim, tt = 2 * (128 / G);  // tokens of a CTA: two query tiles
-  const int64_t ntiles = (static_cast<int64_t>(max_q_len) + tt - 1) / tt;
-  if (num_seqs > 65535 || ntiles > 65535) return PA_ERR_UNSUPPORTED;
-  PrefillArgs a = {};
-  a.q = q;
+  const int64_t pairs = (static_cast<int64_t>(max_q_len) + tt - 1) / tt;
+  if (num_seqs > 65535 || pairs > 65535) return PA_ERR_UNSUPPORTED;
+  WindowArgs a;
+  a.q = static_cast<const __nv_bfloat16*>(q);
   a.cu_q = cu_q_lens;
   a.tables = block_tables;
   a.lens = context_lens;
+  a.sinks = options ? options->sinks : nullptr;
+  a.out = static_cast<__nv_bfloat16*>(out);
+  a.lse = options ? options->lse : nullptr;
   a.num_blocks = cache->num_blocks;
   a.num_seqs = num_seqs;
+  a.num_tokens = num_tokens;
+  a.max_q = max_q_len;
   a.hq = num_q_heads;
   a.hkv = cache->num_kv_heads;
   a.bs = cache->block_size;
   a.max_blocks = max_blocks_per_seq;
   a.max_ctx = max_context_len;
-  a.ntiles = static_cast<int32_t>(ntiles);
-  a.out16 = static_cast<__nv_bfloat16*>(out);
-  a.num_tokens = num_tokens;
-  a.max_q = max_q_len;
   a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
+  a.bshift = cache->block_size == 8 ? 3 : (cache->block_size == 16 ? 4 : 5);
+  const int32_t window = options ? options->window : 0;
+  a.window = window > 0 && window < max_context_len ? window : max_context_len;
   constexpr float kLog2e = 1.4426950408889634f;
-  const float ks = f8 ? cache->k_scale : 1.f;
+  const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
   a.scale_log2 = scale * kLog2e * ks;
+  a.cap_log2 = cap * kLog2e;
+  a.cap_k = cap > 0.f ? scale / cap * ks : 0.f;
+  a.cap_arg = 2.f * kLog2e * a.cap_k;
   a.v_scale = f8 ? cache->v_scale : 1.f;
-  a.window = max_context_len;
-  if (options) {
-    a.lse = options->lse;
-    a.sinks = options->sinks;
-    if (options->window > 0 && options->window < max_context_len) a.window = options->window;
-    a.cap_log2 = options->softcap * kLog2e;
-    a.cap_k = options->softcap > 0.f ? scale / options->softcap * ks : 0.f;
-    a.cap_arg = 2.f * kLog2e * a.cap_k;
-  }
   CUtensorMap tk, tv, tq;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
   auto enc = f8 ? encode_rows_u8 : encode_rows;
   if (!enc(&tk, cache->k, rows, D, cache->block_size) || !enc(&tv, cache->v, rows, D, cache->block_size) ||
       !encode_q_tiles(&tq, const_cast<void*>(q), static_cast<uint64_t>(num_tokens), num_q_heads, D, G))
     return PA_ERR_CUDA;
-  const dim3 grid(cache->num_kv_heads, num_seqs, static_cast<unsigned>(ntiles));
+  const dim3 grid(cache->num_kv_heads, num_seqs, static_cast<unsigned>(pairs));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   auto by_dim = [&](auto cf) -> pa_status {
     constexpr int CF = decltype(cf)::value;

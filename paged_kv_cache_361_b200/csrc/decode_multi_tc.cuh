@@ -352,7 +352,10 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
           float alpha;
           bool resc;
           uint32_t ph[CW / 2];
-          row_weights(a, x, amax, poly, m, l, alpha, resc, ph);
+          if (a.cap_log2 > 0.f)
+            row_weights<true>(a, x, amax, poly, m, l, alpha, resc, ph);
+          else
+            row_weights<false>(a, x, 0.f, poly, m, l, alpha, resc, ph);
           uint32_t pw[C / 2];  // the weights of the half's 64 keys: zeros where another replica has them
 #pragma unroll
           for (int c = 0; c < C / 2; ++c) pw[c] = RF == 1 || c / (CW / 2) == rep ? ph[c % (CW / 2)] : 0u;

@@ -51,16 +51,6 @@ struct PrefillArgs {
   int32_t prefix_part_tokens, max_parts, parts_stride;
   float* ws_ml;
   float* ws_o;
-  // pa_prefill_window (see prefill_tc_kernel's OPT)
-  __nv_bfloat16* out16 = nullptr;  // [num_tokens][hq][D], in place of out
-  float* lse = nullptr;            // [num_tokens][hq] or null
-  const float* sinks = nullptr;    // [hq] or null
-  int32_t num_tokens = 0, max_q = 0;
-  int32_t gshift = 0;              // log2 of hq / hkv
-  int32_t window = 0;              // >= 1; max_ctx or more: every earlier key
-  float cap_log2 = 0.f;            // softcap * log2 e, 0: none
-  float cap_k = 0.f;               // with a cap: scale / softcap (times the K scale)
-  float cap_arg = 0.f;             // 2 log2 e * cap_k
 };
 
 // d += A(16x16) * B(16x8), all 16 rows live.

@@ -58,19 +58,10 @@
 // Q is rounded to f16 by the softmax warps as they stage it (exact for
 // 2^-17 <= |q| <= 65504). The K scale is folded into the score scale; the V
 // scale multiplies O in the final division.
-//
-// OPT (pa_prefill_window): a sliding window, capped scores, sinks, the
-// log-sum-exp of every row, and O rounded once to bf16. The key stream then
-// starts at the chunk of the first key the CTA's first row sees, and each tile
-// joins it at the chunk of its own (jb[t]); blocks before the first seen key
-// are not read and their V rows are written as zeros. A row may see nothing in
-// its tile's first chunks: its maximum stays -inf and its weights are 0. O is
-// half as wide and goes out through shared memory for every tile.
 #pragma once
 
 #include "decode_f8.cuh"
 #include "prefill_mma.cuh"
-#include "score_rule.cuh"
 #include "tcgen05.cuh"
 
 namespace pa {
@@ -162,20 +153,14 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 // TILES query tiles of one (kv head, sequence) per CTA share the K/V stream;
 // tile t is processed by softmax warpgroup t.
 // CF = 0: bf16 cache; kCodeE4M3 / kCodeS8: an 8-bit cache of that format.
-// G: query heads of a kv head (OPT: 0, it is an argument).
-template <int D, int G, int TILES, int CF = 0, bool OPT = false>
+template <int D, int G, int TILES, int CF = 0>
 __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     prefill_tc_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const __grid_constant__ CUtensorMap tmo, const __grid_constant__ CUtensorMap tmq,
                       const PrefillArgs a) {
   constexpr bool F8 = CF != 0;
   using Cfg = TcCfg<D, TILES, F8>;
-  constexpr int S = Cfg::kStages, C = Cfg::kChunk;
-  static_assert(G > 0 || OPT, "the group size is an argument in the OPT form alone");
-  const int GG = G > 0 ? G : 1 << a.gshift;   // query heads of a kv head
-  const int TT = G > 0 ? Cfg::kRows / (G > 0 ? G : 1) : Cfg::kRows >> a.gshift;             // tokens of a tile
-  auto tok_of = [&](int row) { return G > 0 ? row / (G > 0 ? G : 1) : row >> a.gshift; };
-  auto head_of = [&](int row) { return G > 0 ? row % (G > 0 ? G : 1) : row & (GG - 1); };
+  constexpr int S = Cfg::kStages, C = Cfg::kChunk, TT = Cfg::kRows / G;
   constexpr int CS = F8 ? Cfg::kCodeStages : 1;
 
   extern __shared__ uint8_t smem_raw[];
@@ -215,28 +200,19 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     L = L < 0 ? 0 : (L > a.max_ctx ? a.max_ctx : L);
     n = n < 0 ? 0 : (n > L ? L : n);
   }
-  if (OPT && (q0 < 0 || n > a.max_q || q0 > a.num_tokens - n)) {  // left out
-    if (tid == 0 && g == 0 && pair == 0) record_error(PA_ERR_DEVICE_BOUNDS, n);
-    n = 0;
-  }
   const int32_t base = L - n;  // position of new token 0
   const int32_t tok00 = pair * TILES * TT;
   if (tok00 >= n) return;
   // per tile: first token, key end, chunks; the stream follows the last active tile
   int ntiles_act = 0, nch[TILES];
   int32_t kend_all = 0;
-  // OPT: the first key any row sees, its chunk, and every tile's first chunk in the stream
-  const int32_t klo_all = OPT ? max(0, base + tok00 - a.window + 1) : 0;
-  const int32_t c_first = klo_all / C;
-  int jb[TILES];
 #pragma unroll
   for (int t = 0; t < TILES; ++t) {
     const int32_t t0 = tok00 + t * TT;
     nch[t] = 0;
-    jb[t] = OPT ? max(0, base + t0 - a.window + 1) / C - c_first : 0;
     if (t0 < n) {
       const int32_t ke = base + min(t0 + TT, n);
-      nch[t] = (ke + C - 1) / C - c_first;
+      nch[t] = (ke + C - 1) / C;
       kend_all = ke;
       ntiles_act = t + 1;
     }
@@ -298,7 +274,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         if (q_by_tma(t)) {
 #pragma unroll
           for (int hf = 0; hf < Cfg::kHalves; ++hf)
-            tma_load_3d(sbase + t * Cfg::kQTileBytes + hf * Cfg::kQHalfBytes, &tmq, hf * 64, g * GG,
+            tma_load_3d(sbase + t * Cfg::kQTileBytes + hf * Cfg::kQHalfBytes, &tmq, hf * 64, g * G,
                         q0 + tok00 + t * TT, &q_full, pol);
         }
     }
@@ -307,7 +283,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
   // (its ids feed the first K/V copies: one memory round trip less at the start)
   TableAhead ta;
   if (warp == Cfg::kProducerWarp || (!F8 && warp == Cfg::kVProducerWarp))
-    ta.init(a.tables + table_row, c_first * C / a.bs, min(a.max_blocks, (kend_all + a.bs - 1) / a.bs), lane);
+    ta.init(a.tables + table_row, 0, min(a.max_blocks, (kend_all + a.bs - 1) / a.bs), lane);
   if (warp == Cfg::kMmaWarp) {
     tc::alloc(smem_u32(&tmem_base_sh), Cfg::kTmemCols);
     tc::relinquish();
@@ -325,11 +301,11 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     for (; i < nchunks; ++i) {
       const int cst = i % CS;
       if (i >= CS && !warp_wait(&cempty[cst], ((i / CS) - 1) & 1, &ps.abort_flag)) break;
-      const int32_t c0 = (c_first + i) * C;
+      const int32_t c0 = i * C;
       const int32_t nb = (min(C, kend_all - c0) + a.bs - 1) / a.bs;  // <= 8 (bs >= 8)
       const int32_t blk = ta.get(c0 / a.bs, nb, lane);
       bool ok = false;
-      if (lane < nb && (!OPT || c0 + (lane + 1) * a.bs > klo_all)) {
+      if (lane < nb) {
         ok = blk >= 0 && blk < a.num_blocks;
         if (!ok) record_error(PA_ERR_DEVICE_BOUNDS, blk);
       }
@@ -355,8 +331,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
       const int cst = i % CS, st = i % S;
       if (!warp_wait(&cfull[cst], (i / CS) & 1, &ps.abort_flag)) break;
       if (i >= S && !warp_wait(&ps.empty[st], ((i / S) - 1) & 1, &ps.abort_flag)) break;
-      const int32_t key = (c_first + i) * C + row;
-      const bool live = key < kend_all && (!OPT || key >= klo_all);  // rows past the last key become zeros
+      const bool live = i * C + row < kend_all;  // rows past the last key become zeros
       const uint8_t* src = cs0g + cst * Cfg::kCodeStageBytes;
       uint8_t* dst = kv0g + st * Cfg::kStageBytes;
       widen_row_half<D, CF, Cfg::kHalfBytes>(src, dst, row, half, live);
@@ -377,8 +352,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     for (int i = 0; i < nchunks; ++i) {
       const int st = i % S;
       if (!warp_wait(&vfull[st], (i / S) & 1, &ps.abort_flag)) break;
-      const int32_t key = (c_first + i) * C + row;
-      const bool live = key < kend_all && (!OPT || key >= klo_all);  // rows past the last key become zeros
+      const bool live = i * C + row < kend_all;  // rows past the last key become zeros
       v_to_f16_inplace<D, Cfg::kHalfBytes>(kv0g + st * Cfg::kStageBytes + Cfg::kTileBytes, row, half, live);
       tc::fence_proxy_async();  // generic-proxy writes -> tensor-core reads
       __syncwarp();
@@ -398,11 +372,11 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     for (; i < nchunks; ++i) {
       const int st = i % S;
       if (i >= S && !warp_wait(&empty[st], ((i / S) - 1) & 1, &ps.abort_flag)) break;
-      const int32_t c0 = (c_first + i) * C;
+      const int32_t c0 = i * C;
       const int32_t nb = (min(C, kend_all - c0) + a.bs - 1) / a.bs;  // <= 8 (bs >= 8)
       const int32_t blk = ta.get(c0 / a.bs, nb, lane);
       bool ok = false;
-      if (lane < nb && (!OPT || c0 + (lane + 1) * a.bs > klo_all)) {
+      if (lane < nb) {
         ok = blk >= 0 && blk < a.num_blocks;
         if (!ok && !is_v) record_error(PA_ERR_DEVICE_BOUNDS, blk);
       }
@@ -432,10 +406,9 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
       const uint64_t vdesc0 =
           tc::smem_desc(kv0 + Cfg::kTileBytes, Cfg::kHalves > 1 ? Cfg::kHalfBytes : 1024, 1024);
       auto issue_s = [&](int t, int j) {
-        const int jl = j - jb[t];  // the tile's own chunk count: its buffers and phases
         const uint64_t qb = qdesc0 + static_cast<uint64_t>((t * Cfg::kQTileBytes) >> 4);
         const uint64_t kb = kdesc0 + static_cast<uint64_t>(((j % S) * Cfg::kStageBytes) >> 4);
-        const uint32_t dst = tmem + t * Cfg::kTileCols + D + (jl & 1) * C;
+        const uint32_t dst = tmem + t * Cfg::kTileCols + D + (j & 1) * C;
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           // 16 dims = 32 B along the swizzled 128-byte row; 64 dims per box column
@@ -443,11 +416,11 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
           const uint32_t offk = static_cast<uint32_t>((kk >> 2) * Cfg::kHalfBytes + (kk & 3) * 32) >> 4;
           tc::mma_ss(dst, qb + offq, kb + offk, kIdS, kk > 0);
         }
-        tc::commit(smem_u32(&s_full[t][jl & 1]));
+        tc::commit(smem_u32(&s_full[t][j & 1]));
       };
       auto issue_pv = [&](int t, int j) -> bool {
-        const int jl = j - jb[t], sb = jl & 1;
-        if (!warp_wait(&p_full[t][sb], (jl >> 1) & 1, &ps.abort_flag)) return false;
+        const int sb = j & 1;
+        if (!warp_wait(&p_full[t][sb], (j >> 1) & 1, &ps.abort_flag)) return false;
         tc::fence_after();
         // V is N-major: 8-key groups 1024 B apart, the two 64-column halves
         // kHalfBytes apart (one half when D = 64: the offset is then unused)
@@ -457,7 +430,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < C / 16; ++ks) {
           const uint64_t bd = vb + static_cast<uint64_t>((ks * 16 * 128) >> 4);
-          tc::mma_ts(to, tp + ks * 8, bd, kIdPV, jl > 0 || ks > 0);
+          tc::mma_ts(to, tp + ks * 8, bd, kIdPV, j > 0 || ks > 0);
         }
         tc::commit(smem_u32(&o_bar[t]));
         if (j == nch[t] - 1) tc::commit(smem_u32(&o_last[t]));
@@ -469,7 +442,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
       if (ok) {
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
-          if (nch[t] > 0 && jb[t] == 0) issue_s(t, 0);
+          if (nch[t] > 0) issue_s(t, 0);
         if constexpr (!F8) tc::commit(smem_u32(&ps.empty[0]));  // K of stage 0 is read once these finish
       }
       for (int j = 0; ok && j < nchunks; ++j) {
@@ -481,7 +454,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
           tc::fence_after();
 #pragma unroll
           for (int t = 0; t < TILES; ++t)
-            if (j + 1 < nch[t] && j + 1 >= jb[t]) issue_s(t, j + 1);
+            if (j + 1 < nch[t]) issue_s(t, j + 1);
           if constexpr (!F8) tc::commit(smem_u32(&ps.empty[(j + 1) % S]));  // K of chunk j+1 released
         }
         if constexpr (!F8) {
@@ -494,7 +467,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         }
 #pragma unroll
         for (int t = 0; t < TILES; ++t)
-          if (ok && j < nch[t] && j >= jb[t]) ok = issue_pv(t, j);
+          if (ok && j < nch[t]) ok = issue_pv(t, j);
         // every tile is done with stage j (bf16: its V; 8-bit: the whole stage)
         if (ok) tc::commit(smem_u32(F8 ? &ps.empty[j % S] : &vempty[j % S]));
       }
@@ -508,15 +481,14 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
     const int t = warp >> 2;
     const int r = tid & 127;
     const int32_t tok0 = tok00 + t * TT;
-    const int mych = nch[t] > 0 ? nch[t] - jb[t] : 0;
-    const int32_t kfirst = (c_first + jb[t]) * C;
+    const int mych = nch[t];
     if (mych > 0) {
       const int32_t tok_end = min(tok0 + TT, n);
-      const int tok = tok0 + tok_of(r);
+      const int tok = tok0 + r / G;
       const bool valid = tok < n;
       const int32_t pos = base + (valid ? tok : tok_end - 1);  // last key the row sees
-      const int h = head_of(r);
-      const int64_t orow = (static_cast<int64_t>(q0) + (valid ? tok : 0)) * a.hq + g * GG + h;
+      const int h = r % G;
+      const int64_t orow = (static_cast<int64_t>(q0) + (valid ? tok : 0)) * a.hq + g * G + h;
       if (!q_by_tma(t)) {
         const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + orow * D);
         uint8_t* qdst = sgen + t * Cfg::kQTileBytes;
@@ -539,7 +511,6 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
       }
       const uint32_t trow = tmem + t * Cfg::kTileCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
       const float sl2 = a.scale_log2;
-      const CapPoly poly(OPT ? a.cap_log2 : 0.f);
       float m_ref = -INFINITY, l = 0.f;  // m_ref in scaled (log2) units
       bool ok = true;
       for (int j = 0; j < mych; ++j) {
@@ -553,53 +524,46 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
         tc::ld32(trow + D + sb * C, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
         tc::ld32(trow + D + sb * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tc::wait_ld();
-        const int32_t k0 = kfirst + j * C;
-        const float amax = OPT && a.cap_log2 > 0.f ? row_amax(sr) : 0.f;
+        const int32_t k0 = j * C;
         float x[C];
+        // the row maximum over 4 independent partial maxima (three-input max:
+        // short dependence chains, one instruction per two scores)
+        float pm[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) pm[u] = -INFINITY;
         // warp-uniform choice: tcgen05.ld/st below need the whole warp converged
-        const int32_t lo = OPT ? pos - a.window + 1 : 0;  // first key the row sees
-        if (__all_sync(0xffffffffu, k0 + C - 1 <= pos && (!OPT || k0 >= lo))) {
+        if (__all_sync(0xffffffffu, k0 + C - 1 <= pos)) {
 #pragma unroll
           for (int c = 0; c < C; ++c) x[c] = __uint_as_float(sr[c]);
         } else {
 #pragma unroll
-          for (int c = 0; c < C; ++c)
-            x[c] = k0 + c <= pos && (!OPT || k0 + c >= lo) ? __uint_as_float(sr[c]) : -INFINITY;
+          for (int c = 0; c < C; ++c) x[c] = k0 + c <= pos ? __uint_as_float(sr[c]) : -INFINITY;
         }
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
+        float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
+        mx *= sl2;  // scale > 0 keeps the order
         float alpha = 1.f;
         bool resc = false;
-        uint32_t ph[C / 2];
-        if constexpr (OPT) {
-          row_weights(a, x, amax, poly, m_ref, l, alpha, resc, ph);
-        } else {
-          // the row maximum over 4 independent partial maxima (three-input max:
-          // short dependence chains, one instruction per two scores)
-          float pm[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u) pm[u] = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
-          float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-          mx *= sl2;  // scale > 0 keeps the order
-          if (mx > m_ref + 8.f) {
-            alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
-            l *= alpha;
-            resc = j > 0;
-            m_ref = mx;
-          }
-          // weights as packed pairs: (x0, x1) * scale - m in one instruction, the
-          // sums in two packed partial sums (short dependence chains)
-          const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_ref, -m_ref);
-          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-          for (int c = 0; c < C / 2; ++c) {
-            const float2 y = ffma2(make_float2(x[2 * c], x[2 * c + 1]), sc2, nm2);
-            const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
-            part[c & 1] = fadd2(part[c & 1], pp);
-            ph[c] = pack_f16(pp.x, pp.y);  // weights <= 2^8
-          }
-          l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
+        if (mx > m_ref + 8.f) {
+          alpha = fast_exp2(m_ref - mx);  // 0 while m_ref is -inf
+          l *= alpha;
+          m_ref = mx;
+          resc = j > 0;
         }
+        uint32_t ph[C / 2];
+        // weights as packed pairs: (x0, x1) * scale - m in one instruction, the
+        // sums in two packed partial sums (short dependence chains)
+        const float2 sc2 = make_float2(sl2, sl2), nm2 = make_float2(-m_ref, -m_ref);
+        float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < C / 2; ++c) {
+          const float2 y = ffma2(make_float2(x[2 * c], x[2 * c + 1]), sc2, nm2);
+          const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+          part[c & 1] = fadd2(part[c & 1], pp);
+          ph[c] = pack_f16(pp.x, pp.y);  // weights <= 2^8
+        }
+        l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
         __syncwarp();
         tc::st32(trow + D + sb * C, ph);
         if (__any_sync(0xffffffffu, resc)) {
@@ -637,54 +601,8 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
       if (ok) ok = warp_wait(&o_last[t], 0, &ps.abort_flag);
       if (ok) {
         tc::fence_after();
-        float inv;
-        if constexpr (OPT) {
-          float lse;
-          inv = finish_row(a.sinks, g * GG + h, m_ref, l, lse) * (F8 ? a.v_scale : 1.f);
-          if (valid && a.lse) a.lse[orow] = lse;
-        } else {
-          inv = (F8 ? a.v_scale : 1.f) / l;
-        }
-        if constexpr (OPT) {
-          // O as bf16 through the tile's Q area, 64 columns (128 bytes) at a time,
-          // as below
-          uint8_t* stg = sgen + t * Cfg::kQTileBytes + (warp & 3) * 32 * 128;
-          const int pc = lane & 7;
-#pragma unroll
-          for (int q = 0; q < D / 64; ++q) {
-            __syncwarp();
-#pragma unroll
-            for (int hh = 0; hh < 2; ++hh) {
-              uint32_t o[32];
-              tc::ld32(trow + q * 64 + hh * 32, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                uint32_t w[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const __nv_bfloat162 b = __floats2bfloat162_rn(__uint_as_float(o[8 * e + 2 * u]) * inv,
-                                                                 __uint_as_float(o[8 * e + 2 * u + 1]) * inv);
-                  w[u] = *reinterpret_cast<const uint32_t*>(&b);
-                }
-                *reinterpret_cast<uint4*>(stg + lane * 128 + (((4 * hh + e) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-              }
-            }
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int rw = 4 * i + (lane >> 3);
-              const int rr = (warp & 3) * 32 + rw;
-              const int32_t tk = tok0 + tok_of(rr);
-              if (tk < n) {
-                const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * GG + head_of(rr);
-                *reinterpret_cast<uint4*>(a.out16 + orr * D + q * 64 + pc * 8) =
-                    *reinterpret_cast<const uint4*>(stg + rw * 128 + ((pc ^ (rw & 7)) << 4));
-              }
-            }
-          }
-        } else if (t == ntiles_act - 1 && tok0 + TT <= n) {
+        const float inv = (F8 ? a.v_scale : 1.f) / l;
+        if (t == ntiles_act - 1 && tok0 + TT <= n) {
           // The last tile, all rows valid: its last P V was the CTA's last MMA,
           // so the K/V stages are free. O goes there as D / 32 boxes of
           // [128 rows x 32 columns] fp32 in the TMA's 128-byte swizzle, and one
@@ -711,7 +629,7 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
             if (warp_wait(&o_staged, 0, &ps.abort_flag) && lane == 0) {
 #pragma unroll
               for (int q = 0; q < D / 32; ++q)
-                tma_store_3d(&tmo, smem_u32(stg) + q * (128 * 128), q * 32, g * GG, q0 + tok0);
+                tma_store_3d(&tmo, smem_u32(stg) + q * (128 * 128), q * 32, g * G, q0 + tok0);
               bulk_commit();
               bulk_wait_read();
             }
@@ -742,9 +660,9 @@ __global__ void __launch_bounds__(TcCfg<D, TILES, CF != 0>::kThreads, 1)
           for (int i = 0; i < 8; ++i) {
             const int rw = 4 * i + (lane >> 3);         // row within the warp's 32
             const int rr = (warp & 3) * 32 + rw;        // row within the tile
-            const int32_t tk = tok0 + tok_of(rr);
+            const int32_t tk = tok0 + rr / G;
             if (tk < n) {
-              const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * GG + head_of(rr);
+              const int64_t orr = (static_cast<int64_t>(q0) + tk) * a.hq + g * G + rr % G;
               *reinterpret_cast<float4*>(a.out + orr * D + q * 32 + pc * 4) =
                   *reinterpret_cast<const float4*>(stg + rw * 128 + ((pc ^ (rw & 7)) << 4));
             }

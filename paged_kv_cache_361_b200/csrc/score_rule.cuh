@@ -50,7 +50,7 @@ struct CapPoly {
 // score exceeds it by 8, scaling l by alpha and saying whether O has to be
 // scaled too; adds the weights to l and packs them as f16 (they are at most 2^8).
 //   amax: largest |score| of the row, masked ones included (capped scores)
-template <int C, class Args>
+template <bool CAPPED, int C, class Args>
 __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], float amax, const CapPoly& poly,
                                             float& m, float& l, float& alpha, bool& rescale, uint32_t (&ph)[C / 2]) {
   float pm[4];
@@ -59,8 +59,7 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
 #pragma unroll
   for (int c = 0; c < C / 2; ++c) pm[c & 3] = fmax3(pm[c & 3], x[2 * c], x[2 * c + 1]);
   float mx = fmaxf(fmaxf(pm[0], pm[1]), fmaxf(pm[2], pm[3]));
-  const bool capped = a.cap_log2 > 0.f;
-  if (!capped)
+  if (!CAPPED)
     mx *= a.scale_log2;  // scale > 0 keeps the order
   else if (mx != -INFINITY)
     mx = capped_score(mx * a.cap_arg, a.cap_log2);
@@ -85,7 +84,7 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
       ph[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
   };
-  if (!capped) {
+  if constexpr (!CAPPED) {
     const float2 sc2 = make_float2(a.scale_log2, a.scale_log2);
     weigh([&](float2 s) { return ffma2(s, sc2, nm2); });
   } else if (__all_sync(0xffffffffu, amax * a.cap_k <= kCapSmall)) {
