@@ -953,6 +953,7 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.gshift = G == 1 ? 0 : (G == 2 ? 1 : (G == 4 ? 2 : 3));
   a.window = window > 0 && window < max_context_len ? window : (max_context_len > 0 ? max_context_len : 1);
   a.per = plan.per;
+  a.unit_cost = plan.per != 0 ? 0 : (plan.on_tc ? kMultiTcUnitCost : kMultiUnitCost);
   a.slot_rows = plan.rows;
   constexpr float kLog2e = 1.4426950408889634f;
   const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;

@@ -46,6 +46,7 @@ struct MultiArgs {
   int32_t bshift;          // log2 of block_size
   int32_t window;          // >= 1; max_ctx or more: every earlier key
   int32_t per;             // chunks of a worker; 0: even shares, kWholeUnits: a unit each
+  int32_t unit_cost;       // of a unit in an even share, in chunks: see MultiWork
   int32_t slot_rows;       // rows of a partial: max_q hq / hkv
   float scale_log2;        // scale * log2 e (times the K scale of an 8-bit cache)
   float cap_log2;          // softcap * log2 e, 0: none
@@ -92,13 +93,26 @@ __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bo
 // worker; of a unit that does not, each worker leaves a partial (m, l, o): in
 // slot 2w if it is the worker's first segment, in slot 2w + 1 otherwise (it is
 // then the last), and the merge kernel folds them in order. The same lengths give
-// the same shares, so results do not change from call to call.
+// the same shares, so results do not change from call to call. Beginning a unit
+// costs a worker as much as unit_cost chunks (its rows are loaded, the pipeline
+// runs empty and a result is written), so the even shares count each unit as that
+// many chunks more, before its first: a share that begins among them has the unit
+// from its first chunk on, one that ends among them none of it.
 constexpr int32_t kWholeUnits = INT32_MAX;
+
+// Beginning a unit takes a tcgen05 CTA some 6 us, four chunks' time; the three CTAs
+// of an SM of the other kernel hide most of it. Measured at 0 / 2 / 4 / 6 / 8 chunks:
+// 16 sequences of 1000..32768 keys, 5 tokens of 64/8 heads (tcgen05): 208 / 198 /
+// 186 / 184 / 185 us; 32 of 128..2048, 1 to 4 tokens of 32/32 heads over int8: 72 /
+// 62 / 67 / 68 / 72; 64 of 1024..8192, 1 token of 64/8 heads over bf16: 187 / 188 /
+// 190 / 189 / 192.
+constexpr int32_t kMultiUnitCost = 2, kMultiTcUnitCost = 5;
 
 struct MultiWork {
   int32_t s, g, c;   // where the share starts: sequence, kv head, chunk of the unit
   int64_t per;       // chunks of a share
   int64_t left;      // chunks of this one, 0: none
+  int32_t cost;      // the part of `left` that beginning the first unit takes
 };
 
 // The share of worker w of `workers`, at least min_per chunks each; by one warp,
@@ -107,7 +121,7 @@ template <int KEYS>
 __device__ __forceinline__ MultiWork find_work(const MultiArgs& a, int64_t w, int64_t workers, int min_per, bool report) {
   const int lane = threadIdx.x & 31;
   MultiWork k;
-  k.s = k.g = k.c = 0;
+  k.s = k.g = k.c = k.cost = 0;
   if (a.per == kWholeUnits) {
     k.s = static_cast<int32_t>(w / a.hkv);
     k.g = static_cast<int32_t>(w - static_cast<int64_t>(k.s) * a.hkv);
@@ -116,17 +130,21 @@ __device__ __forceinline__ MultiWork find_work(const MultiArgs& a, int64_t w, in
     return k;
   }
   int64_t total = 0;
-  for (int s = lane; s < a.num_seqs; s += 32) total += load_multi_seq(a, s, report && w == 0).chunks(KEYS);
+  for (int s = lane; s < a.num_seqs; s += 32) {
+    const int c = load_multi_seq(a, s, report && w == 0).chunks(KEYS);
+    total += c > 0 ? c + a.unit_cost : 0;
+  }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
   total *= a.hkv;
-  k.per = a.per > 0 ? a.per : max(static_cast<int64_t>(min_per), (total + workers - 1) / workers);
+  k.per = a.per > 0 ? a.per : max(static_cast<int64_t>(min_per + a.unit_cost), (total + workers - 1) / workers);
   const int64_t x = w * k.per;
   k.left = x >= total ? 0 : min(k.per, total - x);
   if (k.left == 0) return k;
-  int64_t base = 0;  // chunks (of one kv head) of the sequences before s0
+  int64_t base = 0;  // chunks and costs (of one kv head) of the sequences before s0
   for (int s0 = 0;; s0 += 32) {
-    const int c = s0 + lane < a.num_seqs ? load_multi_seq(a, s0 + lane, false).chunks(KEYS) : 0;
+    int c = s0 + lane < a.num_seqs ? load_multi_seq(a, s0 + lane, false).chunks(KEYS) : 0;
+    if (c > 0) c += a.unit_cost;
     int64_t upto = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -140,7 +158,9 @@ __device__ __forceinline__ MultiWork find_work(const MultiArgs& a, int64_t w, in
       const int cs = __shfl_sync(0xffffffffu, c, at);
       k.s = s0 + at;
       k.g = static_cast<int32_t>((x - from) / cs);
-      k.c = static_cast<int32_t>(x - from - static_cast<int64_t>(k.g) * cs);
+      const int32_t at_unit = static_cast<int32_t>(x - from - static_cast<int64_t>(k.g) * cs);
+      k.c = max(0, at_unit - a.unit_cost);
+      k.cost = max(0, a.unit_cost - at_unit);
       return k;
     }
     base += __shfl_sync(0xffffffffu, upto, 31);
@@ -165,6 +185,7 @@ struct MultiWalk {
   bool started;
   __device__ __forceinline__ MultiWalk(const MultiWork& work, int64_t worker) : k(work), w(worker), started(false) {}
   __device__ __forceinline__ bool next(const MultiArgs& a, MultiSegment& e) {
+    k.left -= k.cost;
     if (k.left <= 0) return false;
     int32_t cs;
     for (;; ++k.s) {  // a share is left, so some sequence from here on has chunks
@@ -185,6 +206,7 @@ struct MultiWalk {
     started = true;
     k.left -= nc;
     k.c = 0;
+    k.cost = a.unit_cost;
     if (++k.g == a.hkv) {
       k.g = 0;
       ++k.s;
@@ -607,11 +629,11 @@ __global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kern
   e.slot = 0;
   pdl_wait();  // the partials are written by the grid this one was launched behind
   if (k.left == 0 || k.c == 0 || k.c > k.per || rho >= e.rows) return;
-  // worker w - 1 has the first k.c chunks (in its slot 0 if they are all it has),
+  // worker w - 1 has the first k.c chunks (in its slot 0 if the unit is its first),
   // the workers from w on the rest
   const int32_t rest = e.ms.chunks(KEYS) - k.c;
   const int nparts = 1 + static_cast<int>((rest + k.per - 1) / k.per);
-  auto slot = [&](int q) { return (q == 0 ? 2 * (w - 1) + (k.c == k.per ? 0 : 1) : 2 * (w + q - 1)) * a.slot_rows + rho; };
+  auto slot = [&](int q) { return (q == 0 ? 2 * (w - 1) + (k.c + a.unit_cost >= k.per ? 0 : 1) : 2 * (w + q - 1)) * a.slot_rows + rho; };
   float M = -INFINITY;
   for (int q = lane; q < nparts; q += 32) M = fmaxf(M, __ldcg(a.ws_ml + 2 * slot(q)));
   M = warp_max(M);
