@@ -415,8 +415,11 @@ typedef struct {
  *                  may be NULL where that is 0. Its contents need no initial value.
  * q, out and workspace 16-byte aligned. Accumulation is fp32; the result is
  * rounded once to bf16. Over an 8-bit cache q and the weights enter the products
- * as f16. V must be finite at every key that some new token of its sequence sees
- * (a weight of 0 does not hide an infinity or NaN there). Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
+ * as f16 (|q| up to 65504). With max_q_len * num_q_heads / num_kv_heads above 8 the
+ * weights are f16 over a bf16 cache too, and so is V: |V| up to 65504, values
+ * below 2^-14 to a multiple of 2^-24. V must be finite at every key that some new
+ * token of its sequence sees (a weight of 0 does not hide an infinity or NaN
+ * there). Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
  * 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}, max_context_len up to
  * 2^30. Calls sharing a workspace must not overlap on the GPU. options may be
  * NULL: plain causal attention.

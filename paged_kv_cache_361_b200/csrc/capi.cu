@@ -458,10 +458,16 @@ pa_status launch_multi(const MultiArgs& a, const MultiPlan& p, const CUtensorMap
   else
     r = launch(decode_multi_tc_kernel<D, CF, 1>, Tc::kThreads, Tc::kSmemBytes);
   if (r != PA_OK || !p.split) return r;
-  auto merge = p.on_tc ? decode_multi_merge_kernel<D, Tc::kKeys, Tc::kMinChunks>
-                       : decode_multi_merge_kernel<D, Mma::kChunk, Mma::kMinChunks>;
-  const dim3 grid(static_cast<unsigned>(p.workers - 1), (p.rows + kMultiMergeWarps - 1) / kMultiMergeWarps);
-  return launch_kernel(merge, grid, dim3(32 * kMultiMergeWarps), 0, st, true, a);
+  // few units over many workers: many partials a row
+  const int64_t units = static_cast<int64_t>(a.num_seqs) * a.hkv;
+  const bool wide = p.workers >= kMultiWideParts * units;
+  auto merge = p.on_tc ? (wide ? decode_multi_merge_kernel<D, Tc::kKeys, Tc::kMinChunks, true>
+                               : decode_multi_merge_kernel<D, Tc::kKeys, Tc::kMinChunks, false>)
+                       : (wide ? decode_multi_merge_kernel<D, Mma::kChunk, Mma::kMinChunks, true>
+                               : decode_multi_merge_kernel<D, Mma::kChunk, Mma::kMinChunks, false>);
+  const dim3 grid = wide ? dim3(static_cast<unsigned>(units), p.rows)
+                         : dim3(static_cast<unsigned>(p.workers - 1), (p.rows + kMultiMergeWarps - 1) / kMultiMergeWarps);
+  return launch_kernel(merge, grid, dim3(32 * (wide ? kMultiWideWarps : kMultiMergeWarps)), 0, st, true, a, p.workers);
 }
 
 template <int D, int CF>

@@ -115,6 +115,33 @@ struct MultiWork {
   int32_t cost;      // the part of `left` that beginning the first unit takes
 };
 
+// Chunks and costs of one kv head over all sequences and over those before s0, and
+// the length of a share; by one warp, the same in every lane.
+struct MultiSpan {
+  int64_t total, before, per;
+};
+
+template <int KEYS>
+__device__ __forceinline__ MultiSpan multi_span(const MultiArgs& a, int s0, int64_t workers, int min_per,
+                                                bool report = false) {
+  MultiSpan p;
+  p.total = p.before = 0;
+  for (int s = threadIdx.x & 31; s < a.num_seqs; s += 32) {
+    const int c = load_multi_seq(a, s, report).chunks(KEYS);
+    const int x = c > 0 ? c + a.unit_cost : 0;
+    p.total += x;
+    if (s < s0) p.before += x;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    p.total += __shfl_xor_sync(0xffffffffu, p.total, o);
+    p.before += __shfl_xor_sync(0xffffffffu, p.before, o);
+  }
+  p.per = a.per > 0 ? a.per
+                    : max(static_cast<int64_t>(min_per + a.unit_cost), (p.total * a.hkv + workers - 1) / workers);
+  return p;
+}
+
 // The share of worker w of `workers`, at least min_per chunks each; by one warp,
 // the same in every lane.
 template <int KEYS>
@@ -129,15 +156,9 @@ __device__ __forceinline__ MultiWork find_work(const MultiArgs& a, int64_t w, in
     k.left = load_multi_seq(a, k.s, report && k.g == 0 && lane == 0).chunks(KEYS);
     return k;
   }
-  int64_t total = 0;
-  for (int s = lane; s < a.num_seqs; s += 32) {
-    const int c = load_multi_seq(a, s, report && w == 0).chunks(KEYS);
-    total += c > 0 ? c + a.unit_cost : 0;
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  total *= a.hkv;
-  k.per = a.per > 0 ? a.per : max(static_cast<int64_t>(min_per + a.unit_cost), (total + workers - 1) / workers);
+  const MultiSpan sp = multi_span<KEYS>(a, 0, workers, min_per, report && w == 0);
+  const int64_t total = sp.total * a.hkv;
+  k.per = sp.per;
   const int64_t x = w * k.per;
   k.left = x >= total ? 0 : min(k.per, total - x);
   if (k.left == 0) return k;
@@ -607,33 +628,56 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
   pdl_launch_dependents();
 }
 
-// Merge of the units that several workers share: CTA row w looks at the boundary
-// between workers w - 1 and w (grid.x: w from 1, grid.y: rows, a warp each). The
-// first boundary inside a unit merges it, over the partials of worker w - 1 and of
-// those from w on until the unit's end.
-constexpr int kMultiMergeWarps = 4;
+// Merge of the units that several workers share; the first of the `n` partials of a
+// row is worker w's, the others are of the workers after it.
+//
+// kMultiMergeWarps rows a CTA, a warp each: CTA row w looks at the boundary between
+// workers w - 1 and w (grid.x: w from 1, grid.y: rows). The first boundary inside a
+// unit merges it, over the partials of worker w - 1 and of those from w on until the
+// unit's end.
+// WIDE, for few units (grid.x) over many workers: a CTA per unit and row, whose warps
+// share the row's partials. 55 partials of 8 heads one after another took a warp 24
+// us, a third of the whole step over 131072 keys.
+constexpr int kMultiMergeWarps = 4, kMultiWideWarps = 8, kMultiWideParts = 8;
 
-template <int D, int KEYS, int MIN_CHUNKS>
-__global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kernel(const MultiArgs a) {
-  constexpr int VEC = D / 32, U = 4;
-  const int lane = threadIdx.x & 31;
-  const int rho = blockIdx.y * kMultiMergeWarps + (threadIdx.x >> 5);
-  const int64_t w = blockIdx.x + 1;
-  const MultiWork k = find_work<KEYS>(a, w, gridDim.x + 1, MIN_CHUNKS, false);
+template <int D, int KEYS, int MIN_CHUNKS, bool WIDE>
+__global__ void __launch_bounds__(32 * (WIDE ? kMultiWideWarps : kMultiMergeWarps))
+    decode_multi_merge_kernel(const MultiArgs a, int64_t workers) {
+  constexpr int VEC = D / 32, U = 4, NW = WIDE ? kMultiWideWarps : 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rho = WIDE ? blockIdx.y : blockIdx.y * kMultiMergeWarps + warp;
+  int64_t slot0, w;  // slot of the first partial, and the worker after its
+  int nparts;
   MultiSegment e;
-  e.s = k.s;
-  e.g = k.g;
-  e.ms = load_multi_seq(a, k.s, false);
-  e.rows = e.ms.n << a.gshift;
   e.whole = true;
   e.slot = 0;
+  if constexpr (WIDE) {
+    e.s = blockIdx.x / a.hkv;
+    e.g = blockIdx.x - e.s * a.hkv;
+    e.ms = load_multi_seq(a, e.s, false);
+    const int32_t cs = e.ms.chunks(KEYS);
+    const MultiSpan sp = multi_span<KEYS>(a, e.s, workers, MIN_CHUNKS);
+    const int64_t at = sp.before * a.hkv + static_cast<int64_t>(e.g) * (cs + a.unit_cost), x = at + a.unit_cost;
+    w = x / sp.per;
+    nparts = cs > 0 ? static_cast<int>((x + cs - 1) / sp.per - w) + 1 : 0;
+    slot0 = 2 * w + (w * sp.per >= at ? 0 : 1);
+    ++w;
+  } else {
+    w = blockIdx.x + 1;
+    const MultiWork k = find_work<KEYS>(a, w, workers, MIN_CHUNKS, false);
+    e.s = k.s;
+    e.g = k.g;
+    e.ms = load_multi_seq(a, k.s, false);
+    // worker w - 1 has the first k.c chunks (in its slot 0 if the unit is its first),
+    // the workers from w on the rest
+    const int32_t rest = e.ms.chunks(KEYS) - k.c;
+    nparts = k.left == 0 || k.c == 0 || k.c > k.per ? 0 : 1 + static_cast<int>((rest + k.per - 1) / k.per);
+    slot0 = 2 * (w - 1) + (k.c + a.unit_cost >= k.per ? 0 : 1);
+  }
+  e.rows = e.ms.n << a.gshift;
   pdl_wait();  // the partials are written by the grid this one was launched behind
-  if (k.left == 0 || k.c == 0 || k.c > k.per || rho >= e.rows) return;
-  // worker w - 1 has the first k.c chunks (in its slot 0 if the unit is its first),
-  // the workers from w on the rest
-  const int32_t rest = e.ms.chunks(KEYS) - k.c;
-  const int nparts = 1 + static_cast<int>((rest + k.per - 1) / k.per);
-  auto slot = [&](int q) { return (q == 0 ? 2 * (w - 1) + (k.c + a.unit_cost >= k.per ? 0 : 1) : 2 * (w + q - 1)) * a.slot_rows + rho; };
+  if (nparts < 2 || rho >= e.rows) return;
+  auto slot = [&](int q) { return (q == 0 ? slot0 : 2 * (w + q - 1)) * a.slot_rows + rho; };
   float M = -INFINITY;
   for (int q = lane; q < nparts; q += 32) M = fmaxf(M, __ldcg(a.ws_ml + 2 * slot(q)));
   M = warp_max(M);
@@ -641,11 +685,11 @@ __global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kern
 #pragma unroll
   for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
   if (M != -INFINITY) {
-    for (int q0 = 0; q0 < nparts; q0 += U) {  // U partials in flight at a time
+    for (int q0 = WIDE ? warp : 0; q0 < nparts; q0 += U * NW) {  // U partials in flight at a time
       float f[U], lq[U], x[U][VEC];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int64_t row = slot(min(q0 + u, nparts - 1));
+        const int64_t row = slot(min(q0 + u * NW, nparts - 1));
         f[u] = __ldcg(a.ws_ml + 2 * row);
         lq[u] = __ldcg(a.ws_ml + 2 * row + 1);
 #pragma unroll
@@ -653,11 +697,28 @@ __global__ void __launch_bounds__(32 * kMultiMergeWarps) decode_multi_merge_kern
       }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const float wt = q0 + u < nparts ? exp2f(f[u] - M) : 0.f;
+        const float wt = q0 + u * NW < nparts ? exp2f(f[u] - M) : 0.f;
         l = fmaf(lq[u], wt, l);
 #pragma unroll
         for (int i = 0; i < VEC; ++i) acc[i] = fmaf(x[u][i], wt, acc[i]);
       }
+    }
+  }
+  if constexpr (WIDE) {
+    __shared__ float sl[NW], so[NW][D];
+    if (lane == 0) sl[warp] = l;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) so[warp][lane * VEC + i] = acc[i];
+    __syncthreads();
+    if (warp > 0) return;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) acc[i] = 0.f;
+#pragma unroll
+    for (int q = 0; q < NW; ++q) {
+      l += sl[q];
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += so[q][lane * VEC + i];
     }
   }
   float lse;
