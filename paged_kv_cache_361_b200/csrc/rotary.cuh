@@ -17,8 +17,8 @@
 // rotary_dim / 2 later; with neighbours paired, two adjacent pieces. Either way
 // its 8 cosines and 8 sines are adjacent. The rotation is computed in fp32, each
 // operation rounded by itself (no fused multiply-add; in packed pairs, mul and
-// add came out fused), and rounded once to the stored type: for an 8-bit cache the rotated fp32 value is quantised directly,
-// not by way of bf16.
+// add came out fused), and rounded once to the stored type: for an 8-bit cache the
+// rotated fp32 value is quantised directly, not by way of bf16.
 #pragma once
 
 #include "cache_ops.cuh"
@@ -124,14 +124,18 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float2 (&f)[4], fl
 // T: input type; CF: 0 for a cache of the input type, kCodeE4M3 / kCodeS8 for
 // an 8-bit cache. The grid is at most the four CTAs that fit on every SM, walking
 // the tokens: a second wave would cost more than the walk (prompts of 16231
-// tokens, 32 / 32 heads: 146 us, against 167 us at one CTA per token).
+// tokens, 32 / 32 heads: 146 us, against 167 us at one CTA per token). q rows and
+// k, v rows have loops of their own, fewer instructions for each (20011 tokens, 64 /
+// 8 heads over e4m3: 133 us, against 147 us in one loop). Three CTAs with the next
+// row's loads in flight were slower (150 us).
 template <typename T, int CF>
 __global__ void __launch_bounds__(256, 4) rotate_and_cache_kernel(const RotateArgs a) {
   const int32_t D = 16 << a.dshift;
   const int32_t u = threadIdx.x & ((1 << a.dshift) - 1), hr = threadIdx.x >> a.dshift;
-  const int32_t side = hr / a.lanes, lane = hr - side * a.lanes;
+  const int32_t side = hr / a.lanes;
+  int32_t lane = hr - side * a.lanes;
   if (side >= a.tokens) return;
-  const int32_t rows = a.hq + 2 * a.hkv;
+  const int32_t rows = a.hq + 2 * a.hkv, shift = rows % a.lanes;
   // this unit's pieces in a q or k row and in a v row. What is not rotated is
   // taken in halves too, so that neighbouring threads read neighbouring pieces
   const bool turns = 16 * u < a.rd;
@@ -170,82 +174,101 @@ __global__ void __launch_bounds__(256, 4) rotate_and_cache_kernel(const RotateAr
     // element of kv head 0 of the token's slot
     const int64_t blk = slot >> a.bshift;
     const int64_t crow = ((blk * a.hkv) << a.bshift) + (slot - (blk << a.bshift));
-    for (int32_t r = lane; known && r < rows; r += a.lanes) {
-      const bool is_q = r < a.hq, is_v = r >= a.hq + a.hkv;
-      const T* src = is_q   ? static_cast<const T*>(a.q) + t * a.q_stride + r * D
-                     : is_v ? static_cast<const T*>(a.v) + t * a.v_stride + (r - a.hq - a.hkv) * D
-                            : static_cast<const T*>(a.k) + t * a.k_stride + (r - a.hq) * D;
+    // the pairs of two pieces turned, as (p, q) = (p c - q s, q c + p s)
+    auto rotate = [&](float2 (&f0)[4], float2 (&f1)[4]) {
+      auto turn1 = [](float& p, float& q, float c, float s) {
+        const float p0 = p;
+        p = __fsub_rn(__fmul_rn(p0, c), __fmul_rn(q, s));
+        q = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p0, s));
+      };
+      auto turn = [&](float2& p, float2& q, float2 c, float2 s) {
+        turn1(p.x, q.x, c.x, s.x);
+        turn1(p.y, q.y, c.y, s.y);
+      };
+      if (a.interleaved) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {  // pairs 2i, 2i + 1 of each piece: (x, y), (x, y)
+          float2 p = make_float2(f0[2 * i].x, f0[2 * i + 1].x), q = make_float2(f0[2 * i].y, f0[2 * i + 1].y);
+          turn(p, q, co[i], si[i]);
+          f0[2 * i] = make_float2(p.x, q.x);
+          f0[2 * i + 1] = make_float2(p.y, q.y);
+          p = make_float2(f1[2 * i].x, f1[2 * i + 1].x);
+          q = make_float2(f1[2 * i].y, f1[2 * i + 1].y);
+          turn(p, q, co[2 + i], si[2 + i]);
+          f1[2 * i] = make_float2(p.x, q.x);
+          f1[2 * i + 1] = make_float2(p.y, q.y);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn(f0[i], f1[i], co[i], si[i]);
+      }
+    };
+    auto unpack = [](const Piece<T>& x, float2 (&f)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[i] = x.pair(i);
+    };
+    auto pack = [](Piece<T>& x, const float2 (&f)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x.set_pair(i, f[i]);
+    };
+    int32_t r = known ? lane : rows;
+    const T* src = static_cast<const T*>(a.q) + t * a.q_stride + r * D;
+    T* dst = static_cast<T*>(a.q_out) + (t * a.hq + r) * D;
+    for (; r < a.hq; r += a.lanes) {
+      Piece<T> x0, x1;
+      x0.load(src + e0);
+      x1.load(src + e1);
+      if (turns) {
+        float2 f0[4], f1[4];
+        unpack(x0, f0);
+        unpack(x1, f1);
+        rotate(f0, f1);
+        pack(x0, f0);
+        pack(x1, f1);
+      }
+      x0.store(dst + e0);
+      x1.store(dst + e1);
+      src += a.lanes * D;
+      dst += a.lanes * D;
+    }
+    // k and v rows
+    for (; cached && r < rows; r += a.lanes) {
+      const bool is_v = r >= a.hq + a.hkv;
+      const int32_t h = r - a.hq - (is_v ? a.hkv : 0);
+      const T* kv = is_v ? static_cast<const T*>(a.v) + t * a.v_stride + h * D
+                         : static_cast<const T*>(a.k) + t * a.k_stride + h * D;
       const int32_t d0 = is_v ? 8 * u : e0, d1 = is_v ? 8 * u + D / 2 : e1;
       Piece<T> x0, x1;
-      x0.load(src + d0);
-      x1.load(src + d1);
-      float2 f0[4], f1[4];  // the pieces' elements two by two (8-bit: what is quantised)
-      if (CF != 0 || (turns && !is_v)) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f0[i] = x0.pair(i);
-          f1[i] = x1.pair(i);
-        }
-      }
-      if (turns && !is_v) {
-        auto turn1 = [](float& p, float& q, float c, float s) {
-          const float p0 = p;
-          p = __fsub_rn(__fmul_rn(p0, c), __fmul_rn(q, s));
-          q = __fadd_rn(__fmul_rn(q, c), __fmul_rn(p0, s));
-        };
-        auto turn = [&](float2& p, float2& q, float2 c, float2 s) {
-          turn1(p.x, q.x, c.x, s.x);
-          turn1(p.y, q.y, c.y, s.y);
-        };
-        if (a.interleaved) {
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {  // pairs 2i, 2i + 1 of each piece: (x, y), (x, y)
-            float2 p = make_float2(f0[2 * i].x, f0[2 * i + 1].x), q = make_float2(f0[2 * i].y, f0[2 * i + 1].y);
-            turn(p, q, co[i], si[i]);
-            f0[2 * i] = make_float2(p.x, q.x);
-            f0[2 * i + 1] = make_float2(p.y, q.y);
-            p = make_float2(f1[2 * i].x, f1[2 * i + 1].x);
-            q = make_float2(f1[2 * i].y, f1[2 * i + 1].y);
-            turn(p, q, co[2 + i], si[2 + i]);
-            f1[2 * i] = make_float2(p.x, q.x);
-            f1[2 * i + 1] = make_float2(p.y, q.y);
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) turn(f0[i], f1[i], co[i], si[i]);
-        }
-        if (CF == 0 || is_q) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            x0.set_pair(i, f0[i]);
-            x1.set_pair(i, f1[i]);
-          }
-        }
-      }
-      if (is_q) {
-        T* dst = static_cast<T*>(a.q_out) + (t * a.hq + r) * D;
-        x0.store(dst + d0);
-        x1.store(dst + d1);
-        continue;
-      }
-      if (!cached) continue;
-      const int32_t h = r - a.hq - (is_v ? a.hkv : 0);
+      x0.load(kv + d0);
+      x1.load(kv + d1);
       const int64_t row = (crow + (static_cast<int64_t>(h) << a.bshift)) * D;
+      float2 f0[4], f1[4];
+      if (CF != 0 || (turns && !is_v)) {
+        unpack(x0, f0);
+        unpack(x1, f1);
+      }
+      if (turns && !is_v) rotate(f0, f1);
       if constexpr (CF != 0) {
-        uint8_t* dst = static_cast<uint8_t*>(is_v ? a.vc : a.kc) + row;
+        uint8_t* to = static_cast<uint8_t*>(is_v ? a.vc : a.kc) + row;
         const float sc = is_v ? a.v_scale : a.k_scale, rcp = is_v ? a.v_rcp : a.k_rcp;
-        store_codes<CF>(dst + d0, f0, sc, rcp);
-        store_codes<CF>(dst + d1, f1, sc, rcp);
+        store_codes<CF>(to + d0, f0, sc, rcp);
+        store_codes<CF>(to + d1, f1, sc, rcp);
       } else {
-        T* dst = static_cast<T*>(is_v ? a.vc : a.kc) + row;
-        x0.store(dst + d0);
-        x1.store(dst + d1);
+        if (turns && !is_v) {
+          pack(x0, f0);
+          pack(x1, f1);
+        }
+        T* to = static_cast<T*>(is_v ? a.vc : a.kc) + row;
+        x0.store(to + d0);
+        x1.store(to + d1);
       }
     }
     t += stride;
     if (t >= a.num_tokens) return;
     pos = __ldg(a.positions + t);
     slot = __ldg(a.slots + t);
+    // the lanes that took one row less take the first ones now
+    lane += lane < a.lanes - shift ? shift : shift - a.lanes;
   }
 }
 
