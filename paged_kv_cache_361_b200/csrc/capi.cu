@@ -407,11 +407,14 @@ MultiPlan multi_plan(int32_t num_seqs, int32_t max_q_len, int32_t G, int32_t hkv
   p.rows = max_q_len * G;
   p.on_tc = p.rows > 8;
   const int64_t chunk = p.on_tc ? 128 : (f8 ? 128 : 64);
-  int64_t span = max_ctx;  // keys of a unit, from a multiple of 64 on
-  if (window > 0 && static_cast<int64_t>(window) + max_q_len - 1 < span) span = window + max_q_len - 1;
-  span += 63;
-  const int64_t units = static_cast<int64_t>(num_seqs) * hkv, most = (span + chunk - 1) / chunk;
-  if (partition_tokens == 0) {
+  int64_t span = max_ctx;  // keys of a unit: from 0, or from a multiple of 64 before its first window
+  if (window > 0 && static_cast<int64_t>(window) + max_q_len + 62 < span) span = window + max_q_len + 62;
+  const int64_t units = static_cast<int64_t>(num_seqs) * hkv, most = span < chunk ? 1 : (span + chunk - 1) / chunk;
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * (p.on_tc ? 1 : 3);
+  // (even shares of units that all fit, none longer than the least share, are the
+  // units, without a merge launch: 3 sequences of up to 40 keys 12 us, against 14)
+  if (partition_tokens == 0 ||
+      (partition_tokens < 0 && units <= slots && most * chunk <= (p.on_tc ? kMultiTcMinKeys : kMultiMinKeys))) {
     p.per = kWholeUnits;
     p.workers = units;
   } else if (partition_tokens > 0) {
@@ -419,10 +422,9 @@ MultiPlan multi_plan(int32_t num_seqs, int32_t max_q_len, int32_t G, int32_t hkv
     p.workers = (units * most + p.per - 1) / p.per;
   } else {
     p.per = 0;
-    p.workers = static_cast<int64_t>(device_sm_count()) * (p.on_tc ? 1 : 3);
-    if (p.workers > units * most) p.workers = units * most;
+    p.workers = slots < units * most ? slots : units * most;
   }
-  p.split = partition_tokens != 0 && most > 1 && p.workers > 1;
+  p.split = p.per != kWholeUnits && most > 1 && p.workers > 1;
   p.ws_bytes = p.split ? multi_ml_bytes(p) + static_cast<size_t>(2 * p.workers) * p.rows * D * 4 : 0;
   return p;
 }

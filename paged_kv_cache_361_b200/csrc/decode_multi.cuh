@@ -108,6 +108,9 @@ constexpr int32_t kWholeUnits = INT32_MAX;
 // 190 / 189 / 192.
 constexpr int32_t kMultiUnitCost = 2, kMultiTcUnitCost = 5;
 
+// Keys of an even share at least: a smaller one costs more than its part of the work.
+constexpr int32_t kMultiMinKeys = 256, kMultiTcMinKeys = 512;
+
 struct MultiWork {
   int32_t s, g, c;   // where the share starts: sequence, kv head, chunk of the unit
   int64_t per;       // chunks of a share
@@ -305,7 +308,7 @@ struct MultiCfg {
   static constexpr int kStages = 64 * 1024 / kStageBytes;
   static constexpr int kFoldFloats = 32 * (D / 4 + 4);  // one warp's state
   static constexpr int kRowPitch = D + 4;          // floats of a row of the result
-  static constexpr int kMinChunks = 256 / kChunk;  // of a share
+  static constexpr int kMinChunks = kMultiMinKeys / kChunk;
   static constexpr int kSmemBytes = 1024 + kStages * kStageBytes + 2 * kFoldFloats * 4;
   static_assert(8 * (kRowPitch + 2) <= kFoldFloats, "the result takes the place of a state");
 };

@@ -52,7 +52,7 @@ struct MultiTcCfg {
   // half's P in the place of its S
   static constexpr uint32_t kSCol = 2 * D;
   static constexpr int kRowPitch = D + 4;                   // floats of a row in the fold
-  static constexpr int kMinChunks = 4;                      // of a share
+  static constexpr int kMinChunks = kMultiTcMinKeys / kKeys;
   static_assert(kSmemBytes <= 226 * 1024, "shared memory");
   static_assert(128 * (kRowPitch + 2) * 4 <= kStages * kStageBytes, "merge buffer");
 };

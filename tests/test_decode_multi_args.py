@@ -52,7 +52,10 @@ def test_workspace_bytes():
     assert f(4, 4, 1, 32, 8, 128, 1, 0) == 0                              # one chunk a sequence
     assert f(4, 4, 1, 32, 8, 128, 4096, 0) == need(444, 4, 128)           # 3 CTAs per SM
     assert f(20, 4, 5, 32, 8, 128, 4096, 0) == need(148, 20, 128)         # on tcgen05: one
-    assert f(4, 4, 1, 32, 8, 64, 65, 0) == need(4 * 8 * 2, 4, 64)         # fewer chunks than workers: 65 + 63 keys
+    assert f(4, 4, 1, 32, 8, 64, 257, 0) == need(4 * 8 * 5, 4, 64)        # fewer chunks of 64 than workers
+    assert f(4, 4, 1, 32, 8, 64, 256, 0) == 0                             # no unit longer than the least share
+    assert f(4, 4, 1, 32, 8, 64, 0, 0) == 0
+    assert f(60, 60, 1, 64, 8, 64, 256, 0) == need(444, 8, 64)            # but more units than CTAs
     assert f(4, 4, 1, 32, 8, 128, 4096, 1000, 512) == need(4 * 8 * 9 // 4, 4, 128)   # 1000 + 63 keys in 128s, 4 a share
     for bad in ((0, 4, 1, 32, 8, 128, 4096), (4, 4, 17, 32, 8, 128, 4096), (4, 4, 1, 30, 8, 128, 4096),
                 (4, 4, 1, 32, 8, 128, -1), (4, 4, 1, 32, 8, 128, 2 ** 30 + 1)):
