@@ -269,6 +269,22 @@ def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
              _stream_on(dev, stream))
 
 
+def check_rotate(q, k, v, cos_sin, k_cache):
+    """Raises what pa_rotate_and_cache would for these tensors."""
+    dt, hkv, d, dev = input_dtype(k_cache.dtype), k_cache.shape[1], k_cache.shape[3], k_cache.get_device()
+    n, x = int(k.shape[0]), 16 // dt.itemsize
+    if q.dim() != 3:
+        raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
+    for name, t, heads in (("q", q, int(q.shape[1])), ("k", k, hkv), ("v", v, hkv)):
+        if _token_rows(t, name, dt, n, heads, d, dev) % x or t.data_ptr() % 16:
+            raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
+    _on(cos_sin, "cos_sin", torch.float32, 2, dev)
+    if cos_sin.shape[1] < 16 or cos_sin.shape[1] > d or cos_sin.shape[1] % 16:
+        raise PagedAttnError(PA_ERR_UNSUPPORTED, "pa_rotate_and_cache")
+    if q.shape[1] == 0 or cos_sin.data_ptr() % 16:
+        raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
+
+
 def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:
     """cos_sin of pa_rotate_and_cache for the angles position * base^(-2i / rotary_dim),
     computed in 64 bits (a 32-bit product is 4e-3 off at position 10^5)."""

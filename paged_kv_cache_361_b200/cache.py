@@ -160,6 +160,7 @@ class PagedKVCache:
         first = [self.lens.get(s, 0) for s in seq_ids]
         if max((f + c for f, c in zip(first, counts)), default=0) > cos_sin.shape[0]:
             raise ValueError("a sequence outgrew the rotary table")
+        B.check_rotate(q, k, v, cos_sin, self.k_cache)  # before anything changes
         slots = self._extend(seq_ids, counts)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         if len(slots):

@@ -342,7 +342,9 @@ def test_wrong_tensors_are_refused():
                dict(lse=torch.zeros(4, 3, device="cuda")), dict(q=q[:, :, :32]), dict(lse=torch.zeros(4, 4))):
         with pytest.raises((TypeError, ValueError)):
             B.pa_decode_multi(**dict(args, **kw))
-    for kw, st in ((dict(max_q_len=17), B.PA_ERR_UNSUPPORTED), (dict(partition_tokens=64, max_context_len=64), B.PA_ERR_INVALID_ARG),
+    for kw, st in ((dict(max_q_len=17), B.PA_ERR_UNSUPPORTED),
+                   (dict(partition_tokens=64, max_context_len=128, block_tables=torch.zeros(2, 8, dtype=torch.int32).cuda()),
+                    B.PA_ERR_INVALID_ARG),  # two chunks a unit: a workspace is needed
                    (dict(window=-1), B.PA_ERR_INVALID_ARG)):
         with pytest.raises(B.PagedAttnError) as e:
             B.pa_decode_multi(**dict(args, **kw))

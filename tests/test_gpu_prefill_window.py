@@ -256,6 +256,14 @@ def test_cache_calls_are_all_or_nothing():
         with pytest.raises((B.PagedAttnError, ValueError)):
             cache.append_rotated(ids, counts, rows(T, 4), rows(T), rows(T), table)
         assert (dict(cache.lens), cache.bm.stats()) == before
+    good = [rows(2, 4), rows(2), rows(2), table]
+    for i, bad in ((0, good[0].float()), (1, rows(2, 3)), (2, rows(3)), (2, good[2].cpu()), (3, table.double()),
+                   (3, table[:, :24].contiguous()), (3, table[:, :8].contiguous()), (0, rows(2, 0)),
+                   (1, torch.randn(2, 133).bfloat16().cuda()[:, 1:129].view(2, 2, 64)),
+                   (0, torch.randn(2 * 256 + 1).bfloat16().cuda()[1:].view(2, 4, 64))):
+        with pytest.raises((B.PagedAttnError, ValueError, TypeError)):
+            cache.append_rotated([0], [2], *[bad if i == k else x for k, x in enumerate(good)])
+        assert (dict(cache.lens), cache.bm.stats()) == before
     with pytest.raises(ValueError):
         cache.append_rotated([0], [2], rows(3, 4), rows(3), rows(3), table)
     with pytest.raises(ValueError):
