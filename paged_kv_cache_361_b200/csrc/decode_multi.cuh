@@ -463,10 +463,22 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
           // base-2 scores; -inf outside a row's keys (every row sees all of the
           // warp's keys in most chunks)
           if (a.cap_log2 > 0.f) {
+            float amax = 0.f;
 #pragma unroll
             for (int u = 0; u < MT; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x[u][i] = capped_score(x[u][i] * a.cap_arg, a.cap_log2);
+              for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
+            if (__all_sync(0xffffffffu, amax * a.cap_k <= kCapMedium)) {
+#pragma unroll
+              for (int u = 0; u < MT; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][i] = capped_medium(a, x[u][i]);
+            } else {
+#pragma unroll
+              for (int u = 0; u < MT; ++u)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) x[u][i] = capped_score(a, x[u][i]);
+            }
           } else {
 #pragma unroll
             for (int u = 0; u < MT; ++u)

@@ -6,21 +6,30 @@
 
 namespace pa {
 
-// A capped score in base 2, cap_log2 * tanh(y), from z = 2 log2 e * y:
-// tanh(y) = 1 - 2 / (2^z + 1), which is 1 and -1 where 2^z is inf and 0. Its
-// absolute error, a few 2^-24, times a cap of 50 moves a score by 1e-5 at most
-// (the hardware's tanh.approx, at 2^-11, would move it by 2 %).
-__device__ __forceinline__ float capped_score(float z, float cap_log2) {
-  return fmaf(-2.f * cap_log2, __fdividef(1.f, fast_exp2(z) + 1.f), cap_log2);
-}
-
-// The same without exponentials for small y: tanh(y) = y P(y^2), P(z) = 1 + z Q(z),
-// Q of degree 1 or 3 fitted by least squares in Chebyshev polynomials at 400
-// Chebyshev nodes of z. With the fp32 coefficients y P is within 9e-8 of tanh(y)
-// up to 0.2 (degree 1) and within 3e-8 up to 0.5: 6e-6 and 2e-6 for a cap of 50
-// in base 2. Four or six multiply-adds a score, where the exponentials are three
-// operations of a pipe that does one for every eight multiply-adds.
+// tanh of a capped score y = scale s / cap. From z = 2 log2 e * y as 1 - 2 / (2^z +
+// 1), which is 1 and -1 where 2^z is inf and 0, it has an absolute error of a few
+// 2^-24: a cap of 50 makes that 5e-6 of the score, which shows where few keys are
+// seen and the log-sum-exp is small. For small y, and without exponentials, it is
+// y P(y^2), P(z) = 1 + z Q(z), Q of degree 1 or 3 fitted by least squares in Chebyshev
+// polynomials at 400 Chebyshev nodes of z. With the fp32 coefficients y P is within
+// 9e-8 of tanh(y) up to 0.2 (degree 1) and within 3e-8 up to 0.5, with a relative
+// error of a few 2^-24. Four or six multiply-adds a score, where the exponentials are
+// three operations of a pipe that does one for every eight multiply-adds. (The
+// hardware's tanh.approx, at 2^-11, would move a score by 2 %.)
 constexpr float kCapSmall = 0.2f, kCapMedium = 0.5f;
+constexpr float kCapM0 = -0.333333105f, kCapM1 = 0.133305132f, kCapM2 = -0.0533910543f, kCapM3 = 0.0179992188f;
+
+// Capped scores in base 2 from raw ones: |y| up to kCapMedium, and any.
+template <class Args>
+__device__ __forceinline__ float capped_medium(const Args& a, float s) {
+  const float y = s * a.cap_k, z = y * y;
+  return a.cap_log2 * (y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, kCapM3, kCapM2), kCapM1), kCapM0), 1.f));
+}
+template <class Args>
+__device__ __forceinline__ float capped_score(const Args& a, float s) {
+  const float big = a.cap_log2 * fmaf(-2.f, __fdividef(1.f, fast_exp2(s * a.cap_arg) + 1.f), 1.f);
+  return fabsf(s * a.cap_k) <= kCapMedium ? capped_medium(a, s) : big;
+}
 
 // P scaled by cap_log2: the capped score of y in base 2 is y times the value at
 // y^2 (y = -inf gives +inf: a masked score stays -inf).
@@ -33,10 +42,10 @@ struct CapPoly {
     one = cap_log2;
     s[0] = -0.333322763f * cap_log2;
     s[1] = 0.131206915f * cap_log2;
-    m[0] = -0.333333105f * cap_log2;
-    m[1] = 0.133305132f * cap_log2;
-    m[2] = -0.0533910543f * cap_log2;
-    m[3] = 0.0179992188f * cap_log2;
+    m[0] = kCapM0 * cap_log2;
+    m[1] = kCapM1 * cap_log2;
+    m[2] = kCapM2 * cap_log2;
+    m[3] = kCapM3 * cap_log2;
   }
   __device__ __forceinline__ float2 small(float2 y) const { return cap_poly(fmul2(y, y), one, s[0], s[1]); }
   __device__ __forceinline__ float2 medium(float2 y) const {
@@ -62,7 +71,7 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
   if (!CAPPED)
     mx *= a.scale_log2;  // scale > 0 keeps the order
   else if (mx != -INFINITY)
-    mx = capped_score(mx * a.cap_arg, a.cap_log2);
+    mx = capped_score(a, mx);
   alpha = 1.f;
   rescale = false;
   if (mx > m + 8.f) {
@@ -101,8 +110,8 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
     });
   } else {
     weigh([&](float2 s) {
-      return make_float2(s.x == -INFINITY ? -INFINITY : capped_score(s.x * a.cap_arg, a.cap_log2) + nm,
-                         s.y == -INFINITY ? -INFINITY : capped_score(s.y * a.cap_arg, a.cap_log2) + nm);
+      return make_float2(s.x == -INFINITY ? -INFINITY : capped_score(a, s.x) + nm,
+                         s.y == -INFINITY ? -INFINITY : capped_score(a, s.y) + nm);
     });
   }
   l += (part[0].x + part[0].y) + (part[1].x + part[1].y);

@@ -129,6 +129,29 @@ def test_caps_of_every_size(cap, dtype):
     b.check([1, 2], *b.run([1, 2], 8, 70, cap), 70, cap)
 
 
+@pytest.mark.parametrize("cap", [5.0, 30.0, 50.0])
+@pytest.mark.parametrize("n", [1, 8, 40])
+def test_a_capped_score_alone(n, cap):
+    """One key in the window: the log-sum-exp is its capped score, small ones too.
+    q.k are whole numbers and the scale is 1/8, so s is exact. s / cap takes three
+    roundings of 2^-24, tanh six more and a fit within 3e-8 (from 0.5 on: within
+    2^-22 + 2^-23 of 0.46 or more, and its argument's roundings, half as much again),
+    cap log2 e and ln 2 three: under 2^-20 of the value. The weight of the key,
+    2^(x - m) with x and m two roundings apart, and its logarithm: under 2^-22."""
+    g = torch.Generator().manual_seed(n)
+    ints = lambda *s: torch.randint(-3, 4, s, generator=g).float()
+    cache = PagedKVCache(40, 2, 16, 64, torch.bfloat16, "cuda", fill=float("nan"))
+    L = [150, 300, n]
+    q, ks = ints(3 * n, 8, 64), [ints(x, 2, 64) for x in L]
+    for s, k in enumerate(ks):
+        cache.add_sequence(s, k.bfloat16().cuda(), torch.randn(*k.shape, generator=g).bfloat16().cuda())
+    lse = torch.empty(3 * n, 8, device="cuda")
+    cache.attend([0, 1, 2], [n] * 3, q.bfloat16().cuda(), window=1, softcap=cap, lse=lse)
+    k = torch.cat([k[-n:] for k in ks]).double().repeat_interleave(4, 1)
+    want = cap * torch.tanh((q.double() * k).sum(2) / 8 / cap)
+    assert ((lse.cpu().double() - want).abs() <= 2.0 ** -20 * want.abs() + 2.0 ** -22).all()
+
+
 def test_rows_of_no_sequence_stay_and_bad_rows_are_left_out():
     b = Batch([150, 60], 2, 64, 16, "bf16")
     q = torch.randn(200, 4, 64).bfloat16().cuda()
