@@ -373,7 +373,7 @@ pa_status pa_decode_cascade(const void* q, int32_t num_seqs, int32_t num_q_heads
  */
 typedef struct {
   int32_t window;      /* >= 0 */
-  float softcap;       /* >= 0, finite */
+  float softcap;       /* 0, or 2^-40 .. 2^40 */
   const float* sinks;  /* device fp32 [num_q_heads], finite or -inf; NULL: no sink */
   float* lse;          /* device fp32 [num_tokens][num_q_heads], written; NULL: not wanted */
 } pa_attn_options;

@@ -432,7 +432,9 @@ MultiPlan multi_plan(int32_t num_seqs, int32_t max_q_len, int32_t G, int32_t hkv
 // The options of pa_decode_multi and pa_prefill_window.
 pa_status check_options(const pa_attn_options* o) {
   if (!o) return PA_OK;
-  if (o->window < 0 || !std::isfinite(o->softcap) || o->softcap < 0.f) return PA_ERR_INVALID_ARG;
+  // (a cap within 2^+-40: scale / cap and the cap in base 2 stay normal numbers)
+  if (o->window < 0 || !(o->softcap == 0.f || (o->softcap >= 0x1p-40f && o->softcap <= 0x1p40f)))
+    return PA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(o->sinks) & 3) || (reinterpret_cast<uintptr_t>(o->lse) & 3))
     return PA_ERR_INVALID_ARG;
   return PA_OK;

@@ -645,6 +645,8 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
       consumer_bar();  // the buffer is free for the next segment
     }
   }
+  // (at the start it was slower: 54 against 51 us under a window of 1024, 60 against 53
+  // for one sequence of 131072 keys)
   pdl_launch_dependents();
 }
 

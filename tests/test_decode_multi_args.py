@@ -23,7 +23,8 @@ def _call(cache_kw=None, no_options=False, **kw):
 @pytest.mark.parametrize("kw", [
     dict(T=-1), dict(n=-1), dict(mq=0), dict(mq=-3), dict(hq=0), dict(hq=9), dict(mb=0), dict(mc=-1), dict(mc=1025),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(P=-2), dict(P=32),
-    dict(P=100), dict(window=-1), dict(cap=-1.0), dict(cap=float("inf")), dict(cap=float("nan")), dict(sinks=18),
+    dict(P=100), dict(window=-1), dict(cap=-1.0), dict(cap=float("inf")), dict(cap=float("nan")),
+    dict(cap=2.0 ** 41), dict(cap=2.0 ** -41), dict(sinks=18),
     dict(lse=18), dict(q=None), dict(q=24), dict(cu=18), dict(tables=None), dict(tables=18), dict(lens=None),
     dict(lens=18), dict(out=None), dict(out=24), dict(ws=None), dict(ws=128), dict(wsb=64), dict(cu=None),
     dict(cu=None, mq=1, T=2)])

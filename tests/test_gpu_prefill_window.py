@@ -118,7 +118,7 @@ def test_sinks_of_every_size_and_growing_scores():
         _check(b, [300], q, out.cpu(), lse.cpu(), window, cap)
 
 
-@pytest.mark.parametrize("cap", [0.01, 1.5, 5.0, 6.5, 1000.0])
+@pytest.mark.parametrize("cap", [2.0 ** -40, 0.01, 1.5, 5.0, 6.5, 1000.0, 2.0 ** 40])
 @pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
 def test_caps_of_every_size(cap, dtype):
     """From caps that flatten every score, past those where rows are on both

@@ -22,7 +22,8 @@ def _call(cache_kw=None, no_options=False, **kw):
 @pytest.mark.parametrize("kw", [
     dict(T=-1), dict(n=-1), dict(mq=-1), dict(mq=1001), dict(hq=0), dict(hq=9), dict(mb=0), dict(mc=-1), dict(mc=1025),
     dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")), dict(scale=float("inf")), dict(window=-1),
-    dict(cap=-1.0), dict(cap=float("inf")), dict(cap=float("nan")), dict(sinks=18), dict(lse=18), dict(q=None),
+    dict(cap=-1.0), dict(cap=float("inf")), dict(cap=float("nan")),
+    dict(cap=2.0 ** 41), dict(cap=2.0 ** -41), dict(sinks=18), dict(lse=18), dict(q=None),
     dict(q=24), dict(cu=18), dict(cu=None), dict(tables=None), dict(tables=18), dict(lens=None), dict(lens=18),
     dict(out=None), dict(out=24)])
 def test_invalid_arguments(kw):
