@@ -213,6 +213,35 @@ def test_even_shares_over_a_large_ragged_batch():
     assert B.pa_get_device_error()[0] == B.PA_OK
 
 
+@pytest.mark.parametrize("num,hkv,n,window", [(5000, 1, 1, 0), (5000, 2, 3, 40), (700, 8, 16, 0)])
+def test_more_sequences_than_threads(num, hkv, n, window):
+    """Far more units than CTAs, by even shares, by shares of 256 keys and a unit at a
+    time. Two results are each W size (size up to the largest |v|) off before their
+    rounding, and half a step of bf16; two log-sum-exps LSE and a rounding."""
+    g = torch.Generator().manual_seed(num)
+    L = torch.randint(n, 301, (num,), generator=g, dtype=torch.int32)
+    blocks = (L + 15) // 16
+    at = torch.cumsum(blocks, 0) - blocks
+    tables = (at[:, None] + torch.arange(19)).int()       # entries past a sequence's blocks are not used
+    nb = int(blocks.sum())
+    tables[tables >= nb] = -1
+    kc, vc = (torch.randn(nb, hkv, 16, 64, generator=g).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(num * n, 4 * hkv, 64, generator=g).bfloat16().cuda()
+    cu = (torch.arange(num + 1, dtype=torch.int32) * n).cuda()
+    got = []
+    for P in (-1, 0, 256):
+        out, lse = torch.full_like(q, float("nan")), torch.full(q.shape[:2], float("nan"), device="cuda")
+        need = B.pa_decode_multi_workspace_bytes(num * n, num, n, 4 * hkv, hkv, 64, 300, window, P)
+        B.pa_decode_multi(q, cu, kc, vc, tables.cuda(), L.cuda(), 0.125, out, n, 300, window=window, lse=lse,
+                          partition_tokens=P, workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+        got.append((out.double(), lse.double()))
+    assert B.pa_get_device_error()[0] == B.PA_OK
+    top = float(vc.abs().max())
+    for out, lse in got[::2]:
+        assert ((out - got[1][0]).abs() <= 2.0 ** -8 * (out.abs() + got[1][0].abs()) + 2 * W * top).all()
+        assert ((lse - got[1][1]).abs() <= 2 * LSE + 2.0 ** -23 * lse.abs()).all()
+
+
 def test_partitions_agree_and_long_context():
     b = Batch([9000, 4097, 1, 6500], 2, 128, 32, "bf16", seed=5)
     for counts, window in (([1, 1, 1, 1], 0), ([4, 2, 1, 3], 5000), ([4, 4, 1, 16], 0)):
