@@ -417,8 +417,10 @@ typedef struct {
  * rounded once to bf16. Over an 8-bit cache q and the weights enter the products
  * as f16 (|q| up to 65504). With max_q_len * num_q_heads / num_kv_heads above 8 the
  * weights are f16 over a bf16 cache too, and so is V: |V| up to 65504, values
- * below 2^-14 to a multiple of 2^-24. V must be finite at every key that some new
- * token of its sequence sees (a weight of 0 does not hide an infinity or NaN
+ * below 2^-14 to a multiple of 2^-24. A weight as f16 keeps 11 bits down to 2^-21
+ * of its row's largest; below, it is off by at most 2^-32 of the largest: n keys
+ * move the result by at most n 2^-32 max|V|. V must be finite at every key that some
+ * new token of its sequence sees (a weight of 0 does not hide an infinity or NaN
  * there). Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
  * 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}, max_context_len up to
  * 2^30. Calls sharing a workspace must not overlap on the GPU. options may be
@@ -450,7 +452,8 @@ size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int
  *   out            device bf16 [num_tokens][num_q_heads][head_dim]: rounded once.
  *   block_tables   entries of blocks that lie wholly before every window are not
  *                  used (those blocks may have been freed).
- * max_context_len up to 2^30. V must be finite, and up to 65504 in absolute value,
+ * max_context_len up to 2^30. The weights enter the products as f16, with the range
+ * that pa_decode_multi states. V must be finite, and up to 65504 in absolute value,
  * at every key that some new token of its sequence sees: a weight of 0 does not
  * hide an infinity or NaN there from the tile's other rows.
  */

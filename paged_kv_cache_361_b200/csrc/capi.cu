@@ -972,6 +972,7 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.cap_k = cap > 0.f ? scale / cap * ks : 0.f;
   a.cap_arg = 2.f * kLog2e * a.cap_k;
   a.v_scale = f8 ? cache->v_scale : 1.f;
+  a.o_unit = f8 || plan.on_tc ? 1.f / kWeightF16 : 1.f;
   const int D = cache->head_dim;
   CUtensorMap tk, tv;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;

@@ -58,6 +58,7 @@ struct MultiArgs {
   float cap_k;             // with a cap: scale / softcap (times the K scale)
   float cap_arg;           // 2 log2 e * cap_k
   float v_scale;
+  float o_unit;            // of o: 1 / kWeightF16 where the weights are f16, 1 otherwise
 };
 
 // The new rows and length of a sequence, and the start of its chunks.
@@ -292,7 +293,7 @@ __device__ __forceinline__ void store_multi(const MultiArgs& a, const MultiSegme
     return;
   }
   float lse;
-  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), m, l, lse) * a.v_scale;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), m, l, a.o_unit, lse) * a.v_scale;
   const int64_t row = multi_row(a, e, rho);
   const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * f, o.y * f), y1 = __floats2bfloat162_rn(o.z * f, o.w * f);
   *reinterpret_cast<uint2*>(a.out + row * D + d) =
@@ -520,8 +521,8 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
 #pragma unroll
               for (int i = 0; i < 4; ++i) o[t][i] *= alpha[i & 1];
           }
-          // P^T as B fragments (K 16 keys x N 8 rows): f16, or over a bf16 cache a
-          // bf16 and its remainder
+          // P^T as B fragments (K 16 keys x N 8 rows): f16 (times kWeightF16), or over a
+          // bf16 cache a bf16 and its remainder
           uint32_t pb[MT][CF != 0 ? 2 : 4];
           const float ref[2] = {m_run[0] == -INFINITY ? 0.f : m_run[0],   // a row that has seen
                                 m_run[1] == -INFINITY ? 0.f : m_run[1]};  // nothing: weights 0
@@ -532,8 +533,8 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
             l_run[0] += x[u][0] + x[u][2];
             l_run[1] += x[u][1] + x[u][3];
             if constexpr (CF != 0) {
-              pb[u][0] = movmatrix_t(pack_f16(x[u][0], x[u][1]));
-              pb[u][1] = movmatrix_t(pack_f16(x[u][2], x[u][3]));
+              pb[u][0] = movmatrix_t(pack_f16(x[u][0] * kWeightF16, x[u][1] * kWeightF16));
+              pb[u][1] = movmatrix_t(pack_f16(x[u][2] * kWeightF16, x[u][3] * kWeightF16));
             } else {
               uint32_t h01, l01, h23, l23;
               split_pair(x[u][0], x[u][1], h01, l01);
@@ -744,7 +745,7 @@ __global__ void __launch_bounds__(32 * (WIDE ? kMultiWideWarps : kMultiMergeWarp
     }
   }
   float lse;
-  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), M, l, lse) * a.v_scale;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), M, l, a.o_unit, lse) * a.v_scale;
   const int64_t row = multi_row(a, e, rho);
   __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * VEC);
 #pragma unroll

@@ -1,10 +1,20 @@
-// What pa_decode_multi and pa_prefill_window share of their score rule: capped
-// scores, and the end of a row with its sink and log-sum-exp.
+// What pa_decode_multi and pa_prefill_window share of their score rule: the range of
+// the weights, capped scores, and the end of a row with its sink and log-sum-exp.
 #pragma once
 
 #include "common.cuh"
 
 namespace pa {
+
+// Weights that are rounded to f16 for their product with V are packed times 2^7,
+// which o keeps until finish_row. They are 2^(x - m), the running maximum m moving
+// when a score exceeds it by 8, so the largest one packed is between 2^7 and 2^15 of
+// f16's 65504, and a weight keeps its 11 bits down to 2^-21 of the largest; below, it
+// is off by 2^-32 of that at most (n keys together by n 2^-32 max|V| of the result).
+// Without the factor a tail of 33000 keys behind one that outweighs each of them
+// 2^25.5 times was lost whole. (A maximum taken 7 lower costs no multiplication, but
+// rounds the exponents near 7 instead of near 0.)
+constexpr float kWeightF16 = 128.f;
 
 // tanh of a capped score y = scale s / cap. From z = 2 log2 e * y as 1 - 2 / (2^z +
 // 1), which is 1 and -1 where 2^z is inf and 0, it has an absolute error of a few
@@ -57,7 +67,7 @@ struct CapPoly {
 // The weights of a softmax thread's 64 scores x (one row, raw, masked ones
 // -inf), for both tcgen05 kernels: moves the running maximum m (base 2) when a
 // score exceeds it by 8, scaling l by alpha and saying whether O has to be
-// scaled too; adds the weights to l and packs them as f16 (they are at most 2^8).
+// scaled too; adds the weights to l and packs them as f16, times kWeightF16.
 //   amax: largest |score| of the row, masked ones included (capped scores)
 template <bool CAPPED, int C, class Args>
 __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], float amax, const CapPoly& poly,
@@ -89,7 +99,8 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
       const float2 y = score(make_float2(x[2 * c], x[2 * c + 1]));
       const float2 pp = make_float2(fast_exp2(y.x), fast_exp2(y.y));
       part[c & 1] = fadd2(part[c & 1], pp);
-      const __half2 h = __floats2half2_rn(pp.x, pp.y);
+      const float2 ps = fmul2(pp, make_float2(kWeightF16, kWeightF16));
+      const __half2 h = __floats2half2_rn(ps.x, ps.y);
       ph[c] = *reinterpret_cast<const uint32_t*>(&h);
     }
   };
@@ -128,9 +139,9 @@ __device__ __forceinline__ float row_amax(const uint32_t (&s)[C]) {
 }
 
 // The end of a row of head h: (m, l) of all its keys in base 2 with the head's
-// sink, as the factor of o and the log-sum-exp. A row that sees nothing gives
-// 0 and its sink, or -inf.
-__device__ __forceinline__ float finish_row(const float* sinks, int h, float m, float l, float& lse) {
+// sink, as the factor of o (whose weights were packed times 1 / o_unit) and the
+// log-sum-exp. A row that sees nothing gives 0 and its sink, or -inf.
+__device__ __forceinline__ float finish_row(const float* sinks, int h, float m, float l, float o_unit, float& lse) {
   const float sink = sinks ? __ldg(sinks + h) * 1.4426950408889634f : -INFINITY;
   const float M = fmaxf(m, sink);
   if (M == -INFINITY) {
@@ -140,7 +151,7 @@ __device__ __forceinline__ float finish_row(const float* sinks, int h, float m, 
   const float f = exp2f(m - M);
   const float den = l * f + exp2f(sink - M);
   lse = (M + log2f(den)) * 0.6931471805599453f;
-  return f / den;
+  return f / den * o_unit;
 }
 
 }  // namespace pa

@@ -1,0 +1,99 @@
+"""Weights of pa_decode_multi and pa_prefill_window where one key outweighs a long
+tail, against the oracle in 64 bits.
+
+Bounds. Where weights are rounded to f16 (11 bits) they are packed as 2^7 to 2^15
+at the largest, so a weight is off by 2^-11 of itself or by half of f16's least
+step, 2^-25, which is 2^-32 of the largest: over n keys by n 2^-32 max|V| together,
+the denominator being the largest weight at least. Scores are sums of D products in
+fp32, off by at most D 2^-24 sum|q_i k_i| scale: 2e-4 for a sum of 26 (the first
+key's 17.7 and the other dims' 7), so that a weight over the denominator is off by
+2^-12 of itself. V as f16 is off by 2^-25 at most below 2^-14, and the result is
+rounded to bf16 (half a step, 2^-8 of itself).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import fp8, int8
+from oracle.options import options_attention
+from paged_kv_cache_361_b200 import binding as B
+
+pytestmark = pytest.mark.gpu
+
+W = 2.0 ** -11 + 2.0 ** -12
+SCALE = {"bf16": (1.0, 1.0), "e4m3": (0.011, 0.017), "int8": (0.031, 0.027)}
+DT = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+@pytest.fixture(autouse=True)
+def _clean_error_word():
+    B.pa_get_device_error()
+    yield
+
+
+def _paged(rows, dtype, scale):
+    """[L][1][D] fp32 rows as a pool of 32-token blocks in order, and their stored values."""
+    if dtype == "bf16":
+        stored = rows.bfloat16()
+        value = stored.double().numpy()
+    else:
+        q = fp8 if dtype == "e4m3" else int8
+        codes = q.quantize(rows.numpy(), scale)
+        stored, value = torch.from_numpy(codes).view(DT[dtype]), q.dequantize(codes, scale)
+    L, hkv, D = rows.shape
+    raw = stored.view(torch.int16 if dtype == "bf16" else torch.uint8)
+    pool = torch.zeros(-(-L // 32) * 32, hkv, D, dtype=raw.dtype)
+    pool[:L] = raw
+    return pool.view(-1, 32, hkv, D).transpose(1, 2).contiguous().view(DT[dtype]).cuda(), value
+
+
+def _call(kc, vc, q, L, P=None, **rule):
+    """P: partition_tokens of pa_decode_multi, None: pa_prefill_window."""
+    n, hq, D = q.shape
+    tables = torch.arange(kc.shape[0], dtype=torch.int32, device="cuda")[None]
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    lens = torch.tensor([L], dtype=torch.int32, device="cuda")
+    out = torch.empty(n, hq, D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(n, hq, device="cuda")
+    args = (q.cuda(), cu, kc, vc, tables, lens, D ** -0.5, out, n, L)
+    if P is None:
+        B.pa_prefill_window(*args, lse=lse, **rule)
+    else:
+        need = B.pa_decode_multi_workspace_bytes(n, 1, n, hq, kc.shape[1], D, L, rule.get("window", 0), P)
+        B.pa_decode_multi(*args, lse=lse, partition_tokens=P, **rule,
+                          workspace=torch.full((need,), 255, dtype=torch.uint8, device="cuda"))
+    assert B.pa_get_device_error()[0] == B.PA_OK
+    return out.cpu(), lse.cpu()
+
+
+# (new tokens, query heads, partition_tokens): rows on mma.sync, with four, two and one
+# state a row on tcgen05, and pa_prefill_window
+FORMS = [(1, 1, 0), (2, 4, -1), (3, 4, 0), (5, 8, 0), (5, 8, -1), (16, 8, 0), (17, 4, None)]
+
+
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("bf16", 64), ("e4m3", 128), ("int8", 64)])
+@pytest.mark.parametrize("n,hq,P", FORMS)
+@pytest.mark.parametrize("spread", [False, True])
+def test_a_first_key_that_outweighs_a_long_tail(dtype, D, n, hq, P, spread):
+    """The first key has 99.9 % of the weight and a V of 0: the result is that of the
+    tail, 33000 keys of weights next to 2^-25.5 of the first's."""
+    L = 33001
+    g = torch.Generator().manual_seed(n + hq + D)
+    q = torch.randn(n, hq, D, generator=g)
+    q[..., 0] = 64.0
+    K = torch.randn(L, 1, D, generator=g) * (1.0 if spread else 0.0)
+    K[:, :, 0] = 0.0
+    K[0] = 0.0
+    K[0, 0, 0] = 25.5 * np.log(2.0) / 64.0 * D ** 0.5
+    V = 1.0 + 0.25 * torch.randn(L, 1, D, generator=g)
+    V[0] = 0.0
+    q = q.bfloat16()
+    (kc, kv), (vc, vv) = _paged(K, dtype, SCALE[dtype][0]), _paged(V, dtype, SCALE[dtype][1])
+    if dtype != "bf16":
+        B.set_kv_scales(kc, vc, *SCALE[dtype])
+    out, lse = _call(kc, vc, q, L, P)
+    ref, want, size = options_attention(q, kv, vv, D ** -0.5)
+    tol = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * (W * size + L * 2.0 ** -32 * np.abs(vv).max()) + 2.0 ** -24
+    err = np.abs(out.double().numpy() - ref)
+    assert (err <= tol).all(), float((err - tol).max())
+    assert (np.abs(lse.double().numpy() - want) <= 2.0 ** -12 + 2.0 ** -23 * np.abs(want)).all()
