@@ -608,6 +608,8 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
         if (lane == 0) mbar_arrive(&ps.empty[st]);
       }
       sum_l(l_run);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) m_run[h] = final_ref(m_run[h], l_run[h]);
       // fold the warps' states: 2 and 3 into 0 and 1, 1 into 0, then out as rows. A
       // warp that gave up a wait joins every barrier; thread 0 decides for all.
       float* mine = fold + (warp & 1) * Cfg::kFoldFloats + lane * (D / 4 + 4);

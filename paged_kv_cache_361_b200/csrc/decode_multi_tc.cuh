@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t][sb]);
       }
+      m = final_ref(m, l);
       if (ok) ok = warp_wait(&o_last[t], qi & 1, &abort_flag);
       ++qi;
       // fold: half 1 leaves (m, l, o) of its rows in the stages (no MMA or copy

@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
       if (ok && warp_wait(&o_last[t], 0, &abort_flag)) {
       tc::fence_after();
       float lse;
-      const float inv = finish_row(a.sinks, (g << a.gshift) + h, m, l, 1.f / kWeightF16, lse) * a.v_scale;
+      const float inv = finish_row(a.sinks, (g << a.gshift) + h, final_ref(m, l), l, 1.f / kWeightF16, lse) * a.v_scale;
       uint32_t w[D / 2];  // O as bf16
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {

@@ -128,6 +128,11 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
   l += (part[0].x + part[0].y) + (part[1].x + part[1].y);
 }
 
+// The reference of a row at the end of its keys. A maximum skips NaN, so a row whose
+// scores are all NaN (a query of NaN) has kept -inf and would end as one that sees
+// nothing; with a finite reference its NaN of l reaches the result through every merge.
+__device__ __forceinline__ float final_ref(float m, float l) { return l != l ? 0.f : m; }
+
 // Largest |x| of raw scores.
 template <int C>
 __device__ __forceinline__ float row_amax(const uint32_t (&s)[C]) {

@@ -1,7 +1,7 @@
-"""Weights of pa_decode_multi and pa_prefill_window where one key outweighs a long
-tail, against the oracle in 64 bits.
+"""Weights of pa_decode_multi and pa_prefill_window at the ends of their range, in
+every form of the kernels, against the oracle in 64 bits.
 
-Bounds. Where weights are rounded to f16 (11 bits) they are packed as 2^7 to 2^15
+Bounds of the values. Where weights are rounded to f16 (11 bits) they are packed as 2^7 to 2^15
 at the largest, so a weight is off by 2^-11 of itself or by half of f16's least
 step, 2^-25, which is 2^-32 of the largest: over n keys by n 2^-32 max|V| together,
 the denominator being the largest weight at least. Scores are sums of D products in
@@ -97,3 +97,26 @@ def test_a_first_key_that_outweighs_a_long_tail(dtype, D, n, hq, P, spread):
     err = np.abs(out.double().numpy() - ref)
     assert (err <= tol).all(), float((err - tol).max())
     assert (np.abs(lse.double().numpy() - want) <= 2.0 ** -12 + 2.0 ** -23 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,hq,P", FORMS + [(2, 4, 64), (5, 8, 128), (2, 4, 512), (5, 8, 2048)])
+def test_a_query_of_nan_gives_nan(dtype, n, hq, P):
+    """All scores of a row are NaN then: its result is NaN, as by the formula, not
+    that of a row without keys; the other rows keep theirs bit for bit."""
+    L, D = 5000, 64
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn(n, hq, D, generator=g).bfloat16()
+    kc, _ = _paged(torch.randn(L, 1, D, generator=g), dtype, SCALE[dtype][0])
+    vc, _ = _paged(torch.randn(L, 1, D, generator=g), dtype, SCALE[dtype][1])
+    if dtype != "bf16":
+        B.set_kv_scales(kc, vc, *SCALE[dtype])
+    for sinks in (None, torch.zeros(hq, device="cuda")):
+        out, lse = _call(kc, vc, q, L, P, sinks=sinks)
+        bad = q.clone()
+        bad[n - 1, hq // 2] = float("nan")
+        got, got_lse = _call(kc, vc, bad, L, P, sinks=sinks)
+        hit = torch.zeros(n, hq, dtype=torch.bool)
+        hit[n - 1, hq // 2] = True
+        assert got[hit].isnan().all() and got_lse[hit].isnan().all()
+        assert torch.equal(got[~hit], out[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
