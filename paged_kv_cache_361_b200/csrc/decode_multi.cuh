@@ -293,9 +293,11 @@ __device__ __forceinline__ void store_multi(const MultiArgs& a, const MultiSegme
     return;
   }
   float lse;
-  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), m, l, a.o_unit, lse) * a.v_scale;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), m, l, a.o_unit, lse);
+  const float s = a.v_scale;
   const int64_t row = multi_row(a, e, rho);
-  const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * f, o.y * f), y1 = __floats2bfloat162_rn(o.z * f, o.w * f);
+  const __nv_bfloat162 y0 = __floats2bfloat162_rn(o.x * f * s, o.y * f * s),
+                       y1 = __floats2bfloat162_rn(o.z * f * s, o.w * f * s);
   *reinterpret_cast<uint2*>(a.out + row * D + d) =
       make_uint2(*reinterpret_cast<const uint32_t*>(&y0), *reinterpret_cast<const uint32_t*>(&y1));
   if (d == 0 && a.lse) a.lse[row] = lse;
@@ -747,11 +749,11 @@ __global__ void __launch_bounds__(32 * (WIDE ? kMultiWideWarps : kMultiMergeWarp
     }
   }
   float lse;
-  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), M, l, a.o_unit, lse) * a.v_scale;
+  const float f = finish_row(a.sinks, (e.g << a.gshift) + (rho & ((1 << a.gshift) - 1)), M, l, a.o_unit, lse);
   const int64_t row = multi_row(a, e, rho);
   __nv_bfloat162* dst = reinterpret_cast<__nv_bfloat162*>(a.out + row * D + lane * VEC);
 #pragma unroll
-  for (int i = 0; i < VEC / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * f, acc[2 * i + 1] * f);
+  for (int i = 0; i < VEC / 2; ++i) dst[i] = __floats2bfloat162_rn(acc[2 * i] * f * a.v_scale, acc[2 * i + 1] * f * a.v_scale);
   if (lane == 0 && a.lse) a.lse[row] = lse;
 }
 

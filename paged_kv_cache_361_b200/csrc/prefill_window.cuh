@@ -441,7 +441,8 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
       if (ok && warp_wait(&o_last[t], 0, &abort_flag)) {
       tc::fence_after();
       float lse;
-      const float inv = finish_row(a.sinks, (g << a.gshift) + h, final_ref(m, l), l, 1.f / kWeightF16, lse) * a.v_scale;
+      const float inv = finish_row(a.sinks, (g << a.gshift) + h, final_ref(m, l), l, 1.f / kWeightF16, lse);
+      const float vs = F8 ? a.v_scale : 1.f;
       uint32_t w[D / 2];  // O as bf16
 #pragma unroll
       for (int q = 0; q < D / 32; ++q) {
@@ -451,7 +452,7 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const __nv_bfloat162 b =
-              __floats2bfloat162_rn(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+              __floats2bfloat162_rn(__uint_as_float(o[2 * i]) * inv * vs, __uint_as_float(o[2 * i + 1]) * inv * vs);
           w[q * 16 + i] = *reinterpret_cast<const uint32_t*>(&b);
         }
       }

@@ -145,7 +145,9 @@ __device__ __forceinline__ float row_amax(const uint32_t (&s)[C]) {
 
 // The end of a row of head h: (m, l) of all its keys in base 2 with the head's
 // sink, as the factor of o (whose weights were packed times 1 / o_unit) and the
-// log-sum-exp. A row that sees nothing gives 0 and its sink, or -inf.
+// log-sum-exp. A row that sees nothing gives 0 and its sink, or -inf. (A v_scale is
+// multiplied in after the factor: the two together may be below fp32's range where
+// the result is not.)
 __device__ __forceinline__ float finish_row(const float* sinks, int h, float m, float l, float o_unit, float& lse) {
   const float sink = sinks ? __ldg(sinks + h) * 1.4426950408889634f : -INFINITY;
   const float M = fmaxf(m, sink);

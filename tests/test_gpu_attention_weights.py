@@ -120,3 +120,23 @@ def test_a_query_of_nan_gives_nan(dtype, n, hq, P):
         hit[n - 1, hq // 2] = True
         assert got[hit].isnan().all() and got_lse[hit].isnan().all()
         assert torch.equal(got[~hit], out[~hit]) and torch.equal(got_lse[~hit], lse[~hit])
+
+
+@pytest.mark.parametrize("dtype", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,hq,P", FORMS + [(2, 4, 64), (5, 8, 512)])
+def test_a_small_v_scale_keeps_its_bits(dtype, n, hq, P):
+    """A v_scale of 2^-126, fp32's least normal number: the results, means of 4999
+    values of 2^-120 or so, are normal numbers again, and v_scale being a power of
+    two they are those of v_scale 1 times 2^-126 bit for bit."""
+    L, D = 4999, 64
+    g = torch.Generator().manual_seed(n)
+    q = torch.randn(n, hq, D, generator=g).bfloat16()
+    k_scale = SCALE[dtype][0]
+    kc, _ = _paged(torch.randn(L, 1, D, generator=g), dtype, k_scale)
+    vc, _ = _paged(80.0 + 20.0 * torch.rand(L, 1, D, generator=g), dtype, 1.0)
+    got = []
+    for v_scale in (1.0, 2.0 ** -126):
+        B.set_kv_scales(kc, vc, k_scale, v_scale)
+        got.append(_call(kc, vc, q, L, P))
+    assert torch.equal(got[0][0].double() * 2.0 ** -126, got[1][0].double())
+    assert torch.equal(got[0][1], got[1][1])
