@@ -346,14 +346,13 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
           }
           tc::wait_ld();
           const int32_t k0 = e.begin + j * CK + t * C + rep * CW;
-          const float amax = a.cap_log2 > 0.f ? row_amax(sr) : 0.f;
-          float x[CW];
+          float x[CW], amax = 0.f;
 #pragma unroll
           for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(sr[c]);
-          if (!__all_sync(0xffffffffu, k0 >= lo && k0 + CW - 1 <= hi)) {
-#pragma unroll
-            for (int c = 0; c < CW; ++c) x[c] = k0 + c >= lo && k0 + c <= hi ? x[c] : -INFINITY;
-          }
+          if (!__all_sync(0xffffffffu, k0 >= lo && k0 + CW - 1 <= hi))
+            amax = masked_amax(x, lo - k0, hi - k0);
+          else if (a.cap_log2 > 0.f)
+            amax = row_amax(x);
           float alpha;
           bool resc;
           uint32_t ph[CW / 2];

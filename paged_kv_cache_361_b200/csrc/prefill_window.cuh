@@ -392,15 +392,16 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
         tc::ld32(trow + D + sb * C + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
         tc::wait_ld();
         const int32_t k0 = first + (jb[t] + j) * C;
-        const float amax = CAPPED ? row_amax(sr) : 0.f;
-        float x[C];
+        float x[C], amax = 0.f;
         // warp-uniform choice: tcgen05.ld/st below need the whole warp converged
         if (__all_sync(0xffffffffu, k0 + C - 1 <= pos && k0 >= lo)) {
 #pragma unroll
           for (int c = 0; c < C; ++c) x[c] = __uint_as_float(sr[c]);
+          if constexpr (CAPPED) amax = row_amax(x);
         } else {
 #pragma unroll
-          for (int c = 0; c < C; ++c) x[c] = k0 + c <= pos && k0 + c >= lo ? __uint_as_float(sr[c]) : -INFINITY;
+          for (int c = 0; c < C; ++c) x[c] = __uint_as_float(sr[c]);
+          amax = masked_amax(x, lo - k0, pos - k0);
         }
         float alpha;
         bool resc;

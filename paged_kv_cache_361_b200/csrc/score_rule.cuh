@@ -68,7 +68,7 @@ struct CapPoly {
 // -inf), for both tcgen05 kernels: moves the running maximum m (base 2) when a
 // score exceeds it by 8, scaling l by alpha and saying whether O has to be
 // scaled too; adds the weights to l and packs them as f16, times kWeightF16.
-//   amax: largest |score| of the row, masked ones included (capped scores)
+//   amax: largest |score| that the row sees (capped scores)
 template <bool CAPPED, int C, class Args>
 __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], float amax, const CapPoly& poly,
                                             float& m, float& l, float& alpha, bool& rescale, uint32_t (&ph)[C / 2]) {
@@ -133,13 +133,25 @@ __device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], 
 // nothing; with a finite reference its NaN of l reaches the result through every merge.
 __device__ __forceinline__ float final_ref(float m, float l) { return l != l ? 0.f : m; }
 
-// Largest |x| of raw scores.
+// Largest |x| of raw scores that the row sees, all of them or (masked_amax, which
+// puts -inf in the place of the others) those of the columns lo .. hi. It chooses the
+// form of the cap, whose last bits differ: bytes that no row sees must not count.
 template <int C>
-__device__ __forceinline__ float row_amax(const uint32_t (&s)[C]) {
+__device__ __forceinline__ float masked_amax(float (&x)[C], int lo, int hi) {
   float m[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int c = 0; c < C / 2; ++c)
-    m[c & 3] = fmax3(m[c & 3], fabsf(__uint_as_float(s[2 * c])), fabsf(__uint_as_float(s[2 * c + 1])));
+  for (int c = 0; c < C; ++c) {
+    const bool seen = c >= lo && c <= hi;
+    if (seen) m[c & 3] = fmaxf(m[c & 3], fabsf(x[c]));
+    x[c] = seen ? x[c] : -INFINITY;
+  }
+  return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+}
+template <int C>
+__device__ __forceinline__ float row_amax(const float (&x)[C]) {
+  float m[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int c = 0; c < C / 2; ++c) m[c & 3] = fmax3(m[c & 3], fabsf(x[2 * c]), fabsf(x[2 * c + 1]));
   return fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
 }
 

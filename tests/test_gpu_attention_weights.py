@@ -140,3 +140,28 @@ def test_a_small_v_scale_keeps_its_bits(dtype, n, hq, P):
         got.append(_call(kc, vc, q, L, P))
     assert torch.equal(got[0][0].double() * 2.0 ** -126, got[1][0].double())
     assert torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n,hq,P", [(2, 4, 64), (3, 4, 0), (5, 8, 0), (5, 8, 128), (16, 8, 0), (17, 4, None), (40, 1, None)])
+@pytest.mark.parametrize("window", [0, 45])
+def test_capped_bits_do_not_depend_on_bytes_that_no_row_sees(n, hq, P, window, D):
+    """Scores small beside the cap; the slots behind the last token, and those before
+    the first window in a block that it starts in, hold zeros, then large values,
+    infinities and NaN."""
+    L = 331
+    g = torch.Generator().manual_seed(n + D)
+    q = torch.randn(n, hq, D, generator=g).bfloat16()
+    kc, _ = _paged(torch.randn(L, 1, D, generator=g), "bf16", 1.0)
+    vc, _ = _paged(torch.randn(L, 1, D, generator=g), "bf16", 1.0)
+    first = max(0, L - n - window + 1) if window else 0
+    got = []
+    for filler in (0.0, 30.0, 3000.0, float("inf"), float("nan")):
+        for pool in (kc, vc):
+            flat = pool.transpose(1, 2).reshape(-1, 1, D)
+            flat[:first] = filler
+            flat[L:] = filler
+            pool.copy_(flat.view(-1, 32, 1, D).transpose(1, 2))
+        got.append(_call(kc, vc, q, L, P, window=window, softcap=50.0))
+    for out, lse in got[1:]:
+        assert torch.equal(out, got[0][0]) and torch.equal(lse, got[0][1])
