@@ -406,7 +406,9 @@ typedef struct {
  *                  gets a zero row and lse = its sink, or -inf.
  *   block_tables   as for pa_decode. Entries of blocks that lie wholly before
  *                  every window are not used (those blocks may have been freed).
- *   scale          > 0.
+ *   scale          > 0. scale log2 e k_scale (k_scale: 1 over a bf16 cache) is a normal
+ *                  fp32 number, or with a softcap scale / softcap k_scale and 2 log2 e
+ *                  times that.
  *   out            device bf16 [num_tokens][num_q_heads][head_dim].
  *   partition_tokens  -1: even shares, as above; 0: no split, a (sequence, kv head)
  *                  each; > 0, a multiple of 64: shares of that many keys (rounded
@@ -447,7 +449,7 @@ size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int
  *                  num_tokens - 1, or are more than max_q_len, is left out and
  *                  recorded (PA_ERR_DEVICE_BOUNDS); rows of no sequence are left
  *                  as they were.
- *   scale          > 0.
+ *   scale          as for pa_decode_multi.
  *   options        NULL: plain causal attention.
  *   out            device bf16 [num_tokens][num_q_heads][head_dim]: rounded once.
  *   block_tables   entries of blocks that lie wholly before every window are not

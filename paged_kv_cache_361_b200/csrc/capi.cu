@@ -432,12 +432,24 @@ MultiPlan multi_plan(int32_t num_seqs, int32_t max_q_len, int32_t G, int32_t hkv
 // The options of pa_decode_multi and pa_prefill_window.
 pa_status check_options(const pa_attn_options* o) {
   if (!o) return PA_OK;
-  // (a cap within 2^+-40: scale / cap and the cap in base 2 stay normal numbers)
   if (o->window < 0 || !(o->softcap == 0.f || (o->softcap >= 0x1p-40f && o->softcap <= 0x1p40f)))
     return PA_ERR_INVALID_ARG;
   if ((reinterpret_cast<uintptr_t>(o->sinks) & 3) || (reinterpret_cast<uintptr_t>(o->lse) & 3))
     return PA_ERR_INVALID_ARG;
   return PA_OK;
+}
+
+// scale, softcap and the K scale of an 8-bit cache as the kernels take them (ScoreScale of
+// score_rule.cuh). Refused unless each product that is used is a normal number: a masked
+// raw score, -inf, times one that has become 0 is NaN.
+bool score_scale(float scale, const pa_attn_options* o, const pa_cache* cache, ScoreScale* out) {
+  constexpr float kLog2e = 1.4426950408889634f;
+  const float ks = is_8bit(cache->dtype) ? cache->k_scale : 1.f, cap = o ? o->softcap : 0.f;
+  out->scale_log2 = scale * kLog2e * ks;
+  out->cap_log2 = cap * kLog2e;
+  out->cap_k = cap > 0.f ? scale / cap * ks : 0.f;
+  out->cap_arg = 2.f * kLog2e * out->cap_k;
+  return cap > 0.f ? std::isnormal(out->cap_k) && std::isnormal(out->cap_arg) : std::isnormal(out->scale_log2);
 }
 
 constexpr int32_t kMaxOptionContext = 1 << 30;  // positions minus windows stay within 32 bits
@@ -478,7 +490,7 @@ template <int D, int CF>
 pa_status launch_prefill_window(const WindowArgs& a, dim3 grid, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CUtensorMap& tq, cudaStream_t st) {
   using Cfg = WindowCfg<D, CF>;
-  auto kern = a.cap_log2 > 0.f ? prefill_window_kernel<D, CF, true> : prefill_window_kernel<D, CF, false>;
+  auto kern = a.score.cap_log2 > 0.f ? prefill_window_kernel<D, CF, true> : prefill_window_kernel<D, CF, false>;
   if (!smem_attrs(reinterpret_cast<const void*>(kern), Cfg::kSmemBytes, false)) return PA_ERR_CUDA;
   kern<<<grid, Cfg::kThreads, Cfg::kSmemBytes, st>>>(tk, tv, tq, a);
   return launched();
@@ -835,7 +847,8 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
   if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * cache->block_size ||
       max_q_len > max_context_len)
     return PA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || scale <= 0.f) return PA_ERR_INVALID_ARG;
+  WindowArgs a;
+  if (!std::isfinite(scale) || scale <= 0.f || !score_scale(scale, options, cache, &a.score)) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || num_tokens == 0 || max_q_len == 0) return PA_OK;
   if (!q || !cu_q_lens || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out) ||
       (reinterpret_cast<uintptr_t>(cu_q_lens) & 3) || (reinterpret_cast<uintptr_t>(block_tables) & 3) ||
@@ -844,7 +857,6 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
   const int D = cache->head_dim, tt = 2 * (128 / G);  // tokens of a CTA: two query tiles
   const int64_t pairs = (static_cast<int64_t>(max_q_len) + tt - 1) / tt;
   if (num_seqs > 65535 || pairs > 65535) return PA_ERR_UNSUPPORTED;
-  WindowArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.cu_q = cu_q_lens;
   a.tables = block_tables;
@@ -865,12 +877,6 @@ pa_status pa_prefill_window(const void* q, int32_t num_tokens, int32_t num_seqs,
   a.bshift = cache->block_size == 8 ? 3 : (cache->block_size == 16 ? 4 : 5);
   const int32_t window = options ? options->window : 0;
   a.window = window > 0 && window < max_context_len ? window : max_context_len;
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
-  a.scale_log2 = scale * kLog2e * ks;
-  a.cap_log2 = cap * kLog2e;
-  a.cap_k = cap > 0.f ? scale / cap * ks : 0.f;
-  a.cap_arg = 2.f * kLog2e * a.cap_k;
   a.v_scale = f8 ? cache->v_scale : 1.f;
   CUtensorMap tk, tv, tq;
   const uint64_t rows = static_cast<uint64_t>(cache->num_blocks) * cache->num_kv_heads * cache->block_size;
@@ -927,7 +933,8 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
     return PA_ERR_UNSUPPORTED;
   if (static_cast<int64_t>(max_context_len) > static_cast<int64_t>(max_blocks_per_seq) * cache->block_size)
     return PA_ERR_INVALID_ARG;
-  if (!std::isfinite(scale) || scale <= 0.f) return PA_ERR_INVALID_ARG;
+  MultiArgs a;
+  if (!std::isfinite(scale) || scale <= 0.f || !score_scale(scale, options, cache, &a.score)) return PA_ERR_INVALID_ARG;
   if (!cu_q_lens && (max_q_len != 1 || num_tokens < num_seqs)) return PA_ERR_INVALID_ARG;
   if (num_seqs == 0 || num_tokens == 0) return PA_OK;
   if (!q || !block_tables || !context_lens || !out || !aligned16(q) || !aligned16(out) ||
@@ -940,7 +947,6 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   if (plan.workers > INT32_MAX) return PA_ERR_UNSUPPORTED;
   if (plan.split && (!workspace || workspace_bytes < plan.ws_bytes || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return PA_ERR_INVALID_ARG;
-  MultiArgs a;
   a.q = static_cast<const __nv_bfloat16*>(q);
   a.cu_q = cu_q_lens;
   a.tables = block_tables;
@@ -965,12 +971,6 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
   a.per = plan.per;
   a.unit_cost = plan.per != 0 ? 0 : (plan.on_tc ? kMultiTcUnitCost : kMultiUnitCost);
   a.slot_rows = plan.rows;
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float ks = f8 ? cache->k_scale : 1.f, cap = options ? options->softcap : 0.f;
-  a.scale_log2 = scale * kLog2e * ks;
-  a.cap_log2 = cap * kLog2e;
-  a.cap_k = cap > 0.f ? scale / cap * ks : 0.f;
-  a.cap_arg = 2.f * kLog2e * a.cap_k;
   a.v_scale = f8 ? cache->v_scale : 1.f;
   a.o_unit = f8 || plan.on_tc ? 1.f / kWeightF16 : 1.f;
   const int D = cache->head_dim;

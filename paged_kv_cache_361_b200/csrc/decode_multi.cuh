@@ -53,10 +53,7 @@ struct MultiArgs {
   int32_t per;             // chunks of a worker; 0: even shares, kWholeUnits: a unit each
   int32_t unit_cost;       // of a unit in an even share, in chunks: see MultiWork
   int32_t slot_rows;       // rows of a partial: max_q hq / hkv
-  float scale_log2;        // scale * log2 e (times the K scale of an 8-bit cache)
-  float cap_log2;          // softcap * log2 e, 0: none
-  float cap_k;             // with a cap: scale / softcap (times the K scale)
-  float cap_arg;           // 2 log2 e * cap_k
+  ScoreScale score;
   float v_scale;
   float o_unit;            // of o: 1 / kWeightF16 where the weights are f16, 1 otherwise
 };
@@ -465,28 +462,28 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
           }
           // base-2 scores; -inf outside a row's keys (every row sees all of the
           // warp's keys in most chunks)
-          if (a.cap_log2 > 0.f) {
+          if (a.score.cap_log2 > 0.f) {
             float amax = 0.f;
 #pragma unroll
             for (int u = 0; u < MT; ++u)
 #pragma unroll
               for (int i = 0; i < 4; ++i) amax = fmaxf(amax, fabsf(x[u][i]));
-            if (__all_sync(0xffffffffu, amax * a.cap_k <= kCapMedium)) {
+            if (__all_sync(0xffffffffu, amax * a.score.cap_k <= kCapMedium)) {
 #pragma unroll
               for (int u = 0; u < MT; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u][i] = capped_medium(a, x[u][i]);
+                for (int i = 0; i < 4; ++i) x[u][i] = capped_medium(a.score, x[u][i]);
             } else {
 #pragma unroll
               for (int u = 0; u < MT; ++u)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) x[u][i] = capped_score(a, x[u][i]);
+                for (int i = 0; i < 4; ++i) x[u][i] = capped_score(a.score, x[u][i]);
             }
           } else {
 #pragma unroll
             for (int u = 0; u < MT; ++u)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) x[u][i] *= a.scale_log2;
+              for (int i = 0; i < 4; ++i) x[u][i] *= a.score.scale_log2;
           }
           const bool inside = key0 >= e.kbeg && key0 + 16 * MT <= e.kend;
           if (!inside || key0 + 16 * MT - 1 > pos0 || key0 <= pos_hi - a.window) {

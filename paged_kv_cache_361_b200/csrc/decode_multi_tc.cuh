@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
     float* stage0 = reinterpret_cast<float*>(sgen + Cfg::kQBytes);  // the fold: rows of O, then (m, l) of each half
     float* stg = stage0 + r * Cfg::kRowPitch;
     float* ml = stage0 + 128 * Cfg::kRowPitch;
-    const CapPoly poly(a.cap_log2);
+    const CapPoly poly(a.score.cap_log2);
     int qi = 0;
     while (walk.next(a, e)) {
       if (e.chunks == 0) {  // rows that see no key
@@ -351,15 +351,15 @@ __global__ void __launch_bounds__(MultiTcCfg<D, CF>::kThreads, 1)
           for (int c = 0; c < CW; ++c) x[c] = __uint_as_float(sr[c]);
           if (!__all_sync(0xffffffffu, k0 >= lo && k0 + CW - 1 <= hi))
             amax = masked_amax(x, lo - k0, hi - k0);
-          else if (a.cap_log2 > 0.f)
+          else if (a.score.cap_log2 > 0.f)
             amax = row_amax(x);
           float alpha;
           bool resc;
           uint32_t ph[CW / 2];
-          if (a.cap_log2 > 0.f)
-            row_weights<true>(a, x, amax, poly, m, l, alpha, resc, ph);
+          if (a.score.cap_log2 > 0.f)
+            row_weights<true>(a.score, x, amax, poly, m, l, alpha, resc, ph);
           else
-            row_weights<false>(a, x, 0.f, poly, m, l, alpha, resc, ph);
+            row_weights<false>(a.score, x, 0.f, poly, m, l, alpha, resc, ph);
           uint32_t pw[C / 2];  // the weights of the half's 64 keys: zeros where another replica has them
 #pragma unroll
           for (int c = 0; c < C / 2; ++c) pw[c] = RF == 1 || c / (CW / 2) == rep ? ph[c % (CW / 2)] : 0u;

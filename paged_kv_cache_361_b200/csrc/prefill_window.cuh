@@ -52,10 +52,7 @@ struct WindowArgs {
   int32_t num_seqs, num_tokens, max_q, hq, hkv, bs, max_blocks, max_ctx;
   int32_t gshift, bshift;  // log2 of hq / hkv and of block_size
   int32_t window;          // >= 1; max_ctx or more: every earlier key
-  float scale_log2;        // scale * log2 e (times the K scale of an 8-bit cache)
-  float cap_log2;          // softcap * log2 e, 0: none
-  float cap_k;             // with a cap: scale / softcap (times the K scale)
-  float cap_arg;           // 2 log2 e * cap_k
+  ScoreScale score;
   float v_scale;
 };
 
@@ -349,7 +346,7 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
     const int t = warp >> 2, r = tid & 127, h = r & ((1 << a.gshift) - 1);
     const uint32_t trow = tmem + t * Cfg::kTileCols + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     uint8_t* stg = sgen + t * Cfg::kQTileBytes + (warp & 3) * 32 * 128;  // (on the way out: q is done with)
-    const CapPoly poly(CAPPED ? a.cap_log2 : 0.f);
+    const CapPoly poly(CAPPED ? a.score.cap_log2 : 0.f);
     const int nch = je[t] - jb[t];
     if (nch > 0) {
       const int32_t tokt = tok0 + t * tt, tok = tokt + (r >> a.gshift);
@@ -406,7 +403,7 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
         float alpha;
         bool resc;
         uint32_t ph[C / 2];
-        row_weights<CAPPED>(a, x, amax, poly, m, l, alpha, resc, ph);
+        row_weights<CAPPED>(a.score, x, amax, poly, m, l, alpha, resc, ph);
         __syncwarp();
         tc::st32(trow + D + sb * C, ph);
         if (__any_sync(0xffffffffu, resc)) {

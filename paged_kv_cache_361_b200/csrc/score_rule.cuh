@@ -16,6 +16,14 @@ namespace pa {
 // rounds the exponents near 7 instead of near 0.)
 constexpr float kWeightF16 = 128.f;
 
+// What a raw score q.k is multiplied by, normal numbers.
+struct ScoreScale {
+  float scale_log2;  // scale * log2 e (times the K scale of an 8-bit cache)
+  float cap_log2;    // softcap * log2 e, 0: none
+  float cap_k;       // with a cap: scale / softcap (times the K scale)
+  float cap_arg;     // 2 log2 e * cap_k
+};
+
 // tanh of a capped score y = scale s / cap. From z = 2 log2 e * y as 1 - 2 / (2^z +
 // 1), which is 1 and -1 where 2^z is inf and 0, it has an absolute error of a few
 // 2^-24: a cap of 50 makes that 5e-6 of the score, which shows where few keys are
@@ -30,13 +38,11 @@ constexpr float kCapSmall = 0.2f, kCapMedium = 0.5f;
 constexpr float kCapM0 = -0.333333105f, kCapM1 = 0.133305132f, kCapM2 = -0.0533910543f, kCapM3 = 0.0179992188f;
 
 // Capped scores in base 2 from raw ones: |y| up to kCapMedium, and any.
-template <class Args>
-__device__ __forceinline__ float capped_medium(const Args& a, float s) {
+__device__ __forceinline__ float capped_medium(const ScoreScale& a, float s) {
   const float y = s * a.cap_k, z = y * y;
   return a.cap_log2 * (y * fmaf(z, fmaf(z, fmaf(z, fmaf(z, kCapM3, kCapM2), kCapM1), kCapM0), 1.f));
 }
-template <class Args>
-__device__ __forceinline__ float capped_score(const Args& a, float s) {
+__device__ __forceinline__ float capped_score(const ScoreScale& a, float s) {
   const float big = a.cap_log2 * fmaf(-2.f, __fdividef(1.f, fast_exp2(s * a.cap_arg) + 1.f), 1.f);
   return fabsf(s * a.cap_k) <= kCapMedium ? capped_medium(a, s) : big;
 }
@@ -69,8 +75,8 @@ struct CapPoly {
 // score exceeds it by 8, scaling l by alpha and saying whether O has to be
 // scaled too; adds the weights to l and packs them as f16, times kWeightF16.
 //   amax: largest |score| that the row sees (capped scores)
-template <bool CAPPED, int C, class Args>
-__device__ __forceinline__ void row_weights(const Args& a, const float (&x)[C], float amax, const CapPoly& poly,
+template <bool CAPPED, int C>
+__device__ __forceinline__ void row_weights(const ScoreScale& a, const float (&x)[C], float amax, const CapPoly& poly,
                                             float& m, float& l, float& alpha, bool& rescale, uint32_t (&ph)[C / 2]) {
   float pm[4];
 #pragma unroll
