@@ -8,6 +8,7 @@ shared library is missing, importing a device entry point raises.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 
 import numpy as np
@@ -192,6 +193,15 @@ def _on(t, name, dtype, ndim, device_index):
         _dev(t, name, dtype, ndim)
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device_index}")
     return t.data_ptr()
+
+
+def _i32(x, name: str) -> int:
+    """x as a 32-bit argument (ctypes keeps the low 32 bits of a larger one)."""
+    if type(x) is not int:
+        x = operator.index(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} = {x} does not fit 32 bits")
+    return x
 
 
 def _call_on(device_index, fn, what, *args):
@@ -413,13 +423,21 @@ def _attn_options(window, softcap, sinks, lse, num_tokens, num_q_heads, device_i
         lp = _on(lse, "lse", torch.float32, 2, device_index)
         if lse.shape != (num_tokens, num_q_heads):
             raise ValueError("lse must be [num_tokens][num_q_heads]")
-    return pa_attn_options(window, softcap, sp, lp)
+    softcap = float(softcap)
+    if softcap != 0.0 and not 2.0 ** -40 <= softcap <= 2.0 ** 40:  # (as pagedattn.h; 1e-46 would be rounded to 0)
+        raise PagedAttnError(PA_ERR_INVALID_ARG, "softcap")
+    return pa_attn_options(_i32(window, "window"), softcap, sp, lp)
 
 
 def pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
                                     max_context_len, window=0, partition_tokens=-1) -> int:
-    return int(_lib().pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads,
-                                                      head_dim, max_context_len, window, partition_tokens))
+    args = (num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, max_context_len, window,
+            partition_tokens)
+    for x in args:
+        if type(x) is not int or not -0x80000000 <= x <= 0x7fffffff:
+            args = [_i32(x, "a size of pa_decode_multi_workspace_bytes") for x in args]
+            break
+    return int(_lib().pa_decode_multi_workspace_bytes(*args))
 
 
 def _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out):
@@ -456,9 +474,9 @@ def pa_decode_multi(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, 
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = _on(workspace, "workspace", workspace.dtype, workspace.dim(), dev), workspace.nbytes
-    _call_on(dev, _lib().pa_decode_multi, "pa_decode_multi", qp, T, n, cp, max_q_len, hq, ctypes.byref(c), tp,
-             block_tables.shape[1], lp, max_context_len, scale, ctypes.byref(opt), op, partition_tokens, ws, ws_bytes,
-             _stream_on(dev, stream))
+    _call_on(dev, _lib().pa_decode_multi, "pa_decode_multi", qp, T, n, cp, _i32(max_q_len, "max_q_len"), hq,
+             ctypes.byref(c), tp, block_tables.shape[1], lp, _i32(max_context_len, "max_context_len"), float(scale),
+             ctypes.byref(opt), op, _i32(partition_tokens, "partition_tokens"), ws, ws_bytes, _stream_on(dev, stream))
 
 
 def pa_prefill_window(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, scale, out, max_q_len,
@@ -470,8 +488,9 @@ def pa_prefill_window(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens
         raise ValueError("cu_q_lens is needed")
     c, dev, T, hq, n, qp, cp, tp, lp, op = _packed_rows(q, cu_q_lens, k_cache, v_cache, block_tables, context_lens, out)
     opt = _attn_options(window, softcap, sinks, lse, T, hq, dev)
-    _call_on(dev, _lib().pa_prefill_window, "pa_prefill_window", qp, T, n, cp, max_q_len, hq, ctypes.byref(c), tp,
-             block_tables.shape[1], lp, max_context_len, scale, ctypes.byref(opt), op, _stream_on(dev, stream))
+    _call_on(dev, _lib().pa_prefill_window, "pa_prefill_window", qp, T, n, cp, _i32(max_q_len, "max_q_len"), hq,
+             ctypes.byref(c), tp, block_tables.shape[1], lp, _i32(max_context_len, "max_context_len"), float(scale),
+             ctypes.byref(opt), op, _stream_on(dev, stream))
 
 
 def pa_decode_cascade_workspace_bytes(num_seqs, num_q_heads, num_kv_heads, head_dim, max_context_len, block_size,
