@@ -38,6 +38,18 @@ class _Staging:
         h.numpy()[...] = arr
         return h.to(self.device, non_blocking=True)
 
+    def reserve(self, *shape):
+        """An upload of at most that shape whose memory is taken now: a function of
+        the array that returns its rows on the device, for once."""
+        h = torch.empty(shape, dtype=self.t_dtype, pin_memory=True)
+        d = torch.empty(shape, dtype=self.t_dtype, device=self.device)
+
+        def send(arr: np.ndarray) -> torch.Tensor:
+            n = len(arr)
+            h.numpy()[:n] = arr
+            return d[:n].copy_(h[:n], non_blocking=True)
+        return send
+
 
 class PagedKVCache:
     def __init__(self, num_blocks: int, num_kv_heads: int, block_size: int, head_dim: int,
@@ -117,10 +129,10 @@ class PagedKVCache:
         B.pa_reshape_and_cache(k, v, self._slots.upload(slots), self.k_cache, self.v_cache)
         return slots, pairs
 
-    def _extend(self, seq_ids, counts) -> np.ndarray:
+    def _extend(self, seq_ids, counts):
         """Slots of counts[i] new tokens for each sequence seq_ids[i] (a new
-        sequence is created; a live one grows, its shared last block copied
-        first), all or nothing."""
+        sequence is created, a live one grows) and the pairs of blocks to copy
+        before they are written (shared last blocks), on the host, all or nothing."""
         if len(set(seq_ids)) != len(seq_ids):
             raise ValueError("seq_ids must be distinct")
         if len(counts) != len(seq_ids) or min(counts, default=0) < 0:
@@ -133,19 +145,17 @@ class PagedKVCache:
                     made.append(s)
             live = [s for s, n in zip(seq_ids, counts) if s in self.lens for _ in range(n)]
             grown, pairs = self.bm.append_slots(live)
-        except B.PagedAttnError:
+        except BaseException:
             for s in made:
                 self.bm.free_seq(s)
             raise
-        if len(pairs):
-            B.pa_copy_blocks(self.k_cache, self.v_cache, self._pairs.upload(pairs))
         at = 0
         for s, n in zip(seq_ids, counts):
             if s in self.lens:
                 slots[s] = grown[at:at + n]
                 at += n
             self.lens[s] = self.lens.get(s, 0) + n
-        return np.concatenate([slots[s] for s in seq_ids]) if len(seq_ids) else np.empty(0, np.int64)
+        return np.concatenate([slots[s] for s in seq_ids]) if len(seq_ids) else np.empty(0, np.int64), pairs
 
     def append_rotated(self, seq_ids, counts, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
                        interleaved: bool = False) -> torch.Tensor:
@@ -160,13 +170,20 @@ class PagedKVCache:
         first = [self.lens.get(s, 0) for s in seq_ids]
         if max((f + c for f, c in zip(first, counts)), default=0) > cos_sin.shape[0]:
             raise ValueError("a sequence outgrew the rotary table")
-        B.check_rotate(q, k, v, cos_sin, self.k_cache)  # before anything changes
-        slots = self._extend(seq_ids, counts)
+        # whatever may be refused or find no memory comes before anything changes: only
+        # copies and launches follow _extend
+        B.check_rotate(q, k, v, cos_sin, self.k_cache)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
-        if len(slots):
-            pos = np.concatenate([np.arange(f, f + c, dtype=np.int32) for f, c in zip(first, counts)])
-            B.pa_rotate_and_cache(q, k, v, self._lens.upload(pos), cos_sin, self._slots.upload(slots), self.k_cache,
-                                  self.v_cache, q_out, interleaved)
+        T = sum(counts)
+        if T == 0:
+            self._extend(seq_ids, counts)
+            return q_out
+        pos = self._lens.upload(np.concatenate([np.arange(f, f + c, dtype=np.int32) for f, c in zip(first, counts)]))
+        send_slots, send_pairs = self._slots.reserve(T), self._pairs.reserve(len(seq_ids), 2)
+        slots, pairs = self._extend(seq_ids, counts)
+        if len(pairs):
+            B.pa_copy_blocks(self.k_cache, self.v_cache, send_pairs(pairs))
+        B.pa_rotate_and_cache(q, k, v, pos, cos_sin, send_slots(slots), self.k_cache, self.v_cache, q_out, interleaved)
         return q_out
 
     def enable_swap(self, num_host_blocks: int):
