@@ -435,7 +435,8 @@ pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, c
                           void* workspace, size_t workspace_bytes, pa_stream stream);
 
 /* Workspace bytes of pa_decode_multi for these sizes, over a cache of any dtype
- * (0 where it cannot split). window as in pa_attn_options. */
+ * (0 where it cannot split), on the device that is current at the query: it depends
+ * on the number of SMs. window as in pa_attn_options. */
 size_t pa_decode_multi_workspace_bytes(int32_t num_tokens, int32_t num_seqs, int32_t max_q_len, int32_t num_q_heads,
                                        int32_t num_kv_heads, int32_t head_dim, int32_t max_context_len,
                                        int32_t window, int32_t partition_tokens);

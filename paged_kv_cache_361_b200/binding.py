@@ -430,13 +430,20 @@ def _attn_options(window, softcap, sinks, lse, num_tokens, num_q_heads, device_i
 
 
 def pa_decode_multi_workspace_bytes(num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim,
-                                    max_context_len, window=0, partition_tokens=-1) -> int:
+                                    max_context_len, window=0, partition_tokens=-1, device=None) -> int:
+    """The workspace of pa_decode_multi on `device`, that of its cache (default: the
+    current one); it depends on the number of SMs."""
     args = (num_tokens, num_seqs, max_q_len, num_q_heads, num_kv_heads, head_dim, max_context_len, window,
             partition_tokens)
     for x in args:
         if type(x) is not int or not -0x80000000 <= x <= 0x7fffffff:
             args = [_i32(x, "a size of pa_decode_multi_workspace_bytes") for x in args]
             break
+    if device is not None:
+        index = torch.device(device).index
+        if index is not None and index != torch.cuda.current_device():
+            with torch.cuda.device(index):
+                return int(_lib().pa_decode_multi_workspace_bytes(*args))
     return int(_lib().pa_decode_multi_workspace_bytes(*args))
 
 

@@ -312,7 +312,7 @@ class PagedKVCache:
             B.pa_prefill_window(*args, **rule)
             return out
         nbytes = B.pa_decode_multi_workspace_bytes(T, len(counts), max(counts), hq, self.k_cache.shape[1], d, max_len,
-                                                   window)
+                                                   window, device=self.k_cache.device)
         B.pa_decode_multi(*args, workspace=self.workspace(nbytes), **rule)
         return out
 
