@@ -82,7 +82,7 @@ class PagedKVCache:
         self._pairs = _Staging(np.int32, torch.int32, self.device)
         self._tables = _Staging(np.int32, torch.int32, self.device)
         self._lens = _Staging(np.int32, torch.int32, self.device)
-        self._ws = None
+        self._ws: dict[int, torch.Tensor] = {}
         self._dev_staging = None
         self._host_staging = None
 
@@ -220,11 +220,15 @@ class PagedKVCache:
         return tables, lens, max_len
 
     def workspace(self, nbytes: int):
+        """At least nbytes of device memory for a call on the current stream, kept for
+        the next one there (calls on two streams may overlap)."""
         if nbytes == 0:
             return None
-        if self._ws is None or self._ws.numel() < nbytes:
-            self._ws = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
-        return self._ws
+        stream = B._stream_on(self.k_cache.get_device(), None)
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < nbytes:
+            ws = self._ws[stream] = torch.empty(nbytes, dtype=torch.uint8, device=self.device)
+        return ws
 
     def decode(self, seq_ids, q: torch.Tensor, scale: float | None = None, out: torch.Tensor | None = None,
                partition_tokens: int = -1, longest_first: bool = True) -> torch.Tensor:

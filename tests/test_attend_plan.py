@@ -57,3 +57,20 @@ def test_attend_plans_for_its_cache_s_device(monkeypatch, host_cache):
     host_cache.k_cache = types.SimpleNamespace(shape=host_cache.k_cache.shape, device=torch.device("cuda:1"))
     host_cache.attend([0], [1], torch.zeros(1, 4, 64, dtype=torch.bfloat16))
     assert asked == [900]
+
+
+def test_streams_do_not_share_a_workspace(monkeypatch, host_cache):
+    """Calls that share one must not overlap on the GPU; those of two streams may."""
+    now = [11]
+    monkeypatch.setattr(B, "_stream_on", lambda *a: now[0])
+    first = host_cache.workspace(1000)
+    assert host_cache.workspace(600) is first and host_cache.workspace(0) is None
+    now[0] = 22
+    other = host_cache.workspace(1000)
+    assert other.data_ptr() != first.data_ptr()
+    larger = host_cache.workspace(5000)
+    assert larger.numel() >= 5000
+    now[0] = 11
+    assert host_cache.workspace(1000) is first
+    now[0] = 22
+    assert host_cache.workspace(1000) is larger
