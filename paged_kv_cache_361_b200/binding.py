@@ -279,19 +279,22 @@ def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
              _stream_on(dev, stream))
 
 
-def check_rotate(q, k, v, cos_sin, k_cache):
+def check_rotate(q, k, v, cos_sin, k_cache, v_cache):
     """Raises what pa_rotate_and_cache would for these tensors."""
-    dt, hkv, d, dev = input_dtype(k_cache.dtype), k_cache.shape[1], k_cache.shape[3], k_cache.get_device()
-    n, x = int(k.shape[0]), 16 // dt.itemsize
+    c = make_cache(k_cache, v_cache)
+    dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
+    n = int(k.shape[0])
     if q.dim() != 3:
         raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
-    for name, t, heads in (("q", q, int(q.shape[1])), ("k", k, hkv), ("v", v, hkv)):
-        if _token_rows(t, name, dt, n, heads, d, dev) % x or t.data_ptr() % 16:
-            raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
+    hq = int(q.shape[1])
+    sq, sk, sv = (_token_rows(t, name, dt, n, heads, d, dev)
+                  for name, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)))
     _on(cos_sin, "cos_sin", torch.float32, 2, dev)
-    if cos_sin.shape[1] < 16 or cos_sin.shape[1] > d or cos_sin.shape[1] % 16:
-        raise PagedAttnError(PA_ERR_UNSUPPORTED, "pa_rotate_and_cache")
-    if q.shape[1] == 0 or cos_sin.data_ptr() % 16:
+    max_positions, rotary_dim = cos_sin.shape
+    # the call without tokens: it checks all but the pointers, and uses none
+    _check(_lib().pa_rotate_and_cache(16, sq, 16, sk, 16, sv, None, None, max(1, max_positions), rotary_dim, 0, None, 0, hq,
+                                      ctypes.byref(c), 32, None), "pa_rotate_and_cache")
+    if n and any(t.data_ptr() % 16 for t in (q, k, v, cos_sin)):
         raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
 
 

@@ -172,7 +172,7 @@ class PagedKVCache:
             raise ValueError("a sequence outgrew the rotary table")
         # whatever may be refused or find no memory comes before anything changes: only
         # copies and launches follow _extend
-        B.check_rotate(q, k, v, cos_sin, self.k_cache)
+        B.check_rotate(q, k, v, cos_sin, self.k_cache, self.v_cache)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
         T = sum(counts)
         if T == 0:

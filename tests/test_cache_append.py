@@ -29,6 +29,7 @@ def layer(monkeypatch):
         return f
     monkeypatch.setattr(B, "pa_rotate_and_cache", lambda *a: calls.append(("rotate", a)))
     monkeypatch.setattr(B, "pa_copy_blocks", lambda *a: calls.append(("copy", a)))
+    monkeypatch.setattr(B, "make_cache", lambda k, v: _struct(k, {}))
     monkeypatch.setattr(cache_module.torch, "empty", allocate(torch.empty))
     cache = PagedKVCache(6, 2, 16, 64, torch.bfloat16, "cpu")
     cache.reserve(0, 30)
@@ -92,3 +93,24 @@ def test_no_blocks_left_changes_nothing(layer):
     with pytest.raises(B.PagedAttnError):
         cache.append_rotated([7, 0], [16, 90], _rows(106, 4), _rows(106), _rows(106), TABLE)
     assert _state(cache) == before and not calls
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(head_dim=96), B.PA_ERR_UNSUPPORTED), (dict(block_size=24), B.PA_ERR_UNSUPPORTED),
+    (dict(dtype=torch.int8, k_scale=0.0), B.PA_ERR_INVALID_ARG),
+    (dict(dtype=torch.float8_e4m3fn, v_scale=float("nan")), B.PA_ERR_INVALID_ARG)])
+def test_a_cache_that_the_native_call_refuses_changes_nothing(monkeypatch, layer, kw, status):
+    args = dict(dict(num_blocks=6, num_kv_heads=2, block_size=16, head_dim=64, dtype=torch.bfloat16, device="cpu"), **kw)
+    cache = PagedKVCache(**args)
+    monkeypatch.setattr(B, "make_cache", lambda k, v: _struct(k, kw))
+    d = args["head_dim"]
+    rows = lambda h: torch.zeros(5, h, d, dtype=torch.bfloat16)
+    with pytest.raises(B.PagedAttnError) as e:
+        cache.append_rotated([0], [5], rows(4), rows(2), rows(2), torch.zeros(20, 64))
+    assert e.value.status == status
+    assert cache.lens == {} and cache.bm.stats()["free_blocks"] == 6
+
+
+def _struct(k_cache, kw):
+    dtype = {torch.bfloat16: B.PA_BF16, torch.int8: B.PA_INT8, torch.float8_e4m3fn: B.PA_FP8_E4M3}[k_cache.dtype]
+    return B.pa_cache(16, 32, *k_cache.shape, dtype, kw.get("k_scale", 1.0), kw.get("v_scale", 1.0))
