@@ -23,10 +23,11 @@
 // read, scores outside a row's window are replaced by -inf, V rows outside [kbeg,
 // kend) are zeroed in registers (a freed block may hold anything, NaN too).
 //
-// Measured: 64 sequences of 1024..8192 keys, 1 token of 64/8 heads: 189 us over bf16,
-// 6.4 TB/s, 0.97 of a copy's rate, 104 us over e4m3 (0.89: the conversions show);
-// 64 of 128..8192 in a window of 1024, 32/8 heads: 51 us, 5.0 TB/s (some 10 us of
-// every call are lengths, first copies and merge).
+// Measured (kernels back to back in a graph, inputs larger than L2, as all figures of
+// this file): 64 sequences of 1024..8192 keys, 1 token of 64/8 heads: 185 to 192 us over
+// bf16, 6.3 to 6.5 TB/s, 0.96 to 0.99 of a copy's rate, 102 to 108 us over e4m3 (0.85 to
+// 0.90: the conversions show); 64 of 128..8192 in a window of 1024, 32/8 heads: 50 us,
+// 5.1 TB/s (some 10 us of every call are lengths, first copies and merge).
 #pragma once
 
 #include "decode_f8.cuh"
@@ -104,14 +105,20 @@ __device__ __forceinline__ MultiSeq load_multi_seq(const MultiArgs& a, int s, bo
 constexpr int32_t kWholeUnits = INT32_MAX;
 
 // Beginning a unit takes a tcgen05 CTA some 6 us, four chunks' time; the three CTAs
-// of an SM of the other kernel hide most of it. Measured at 0 / 2 / 4 / 6 / 8 chunks:
-// 16 sequences of 1000..32768 keys, 5 tokens of 64/8 heads (tcgen05): 208 / 198 /
-// 186 / 184 / 185 us; 32 of 128..2048, 1 to 4 tokens of 32/32 heads over int8: 72 /
-// 62 / 67 / 68 / 72; 64 of 1024..8192, 1 token of 64/8 heads over bf16: 187 / 188 /
-// 190 / 189 / 192.
+// of an SM of the other kernel hide most of it. Measured on tcgen05 at 2 / 5 / 8 chunks:
+// 16 sequences of 1000..32768 keys, 5 tokens of 64/8 heads 209 / 190 / 199 us; 64 of
+// 300..2000, 8 tokens of 16/8 heads 84 / 83 / 91; but 32 of 1024..8192, 3 tokens of
+// 32/8 heads 114 / 130 / 133. On mma.sync at 1 / 2 / 4: 32 of 128..2048, 1 to 4 tokens of
+// 32/32 heads over int8 67 / 66 / 72; 64 of 1024..8192, 1 token of 64/8 heads 188 / 185 /
+// 189 over bf16, 102 / 102 / 104 over e4m3.
 constexpr int32_t kMultiUnitCost = 2, kMultiTcUnitCost = 5;
 
 // Keys of an even share at least: a smaller one costs more than its part of the work.
+// At half / this / twice: on mma.sync, 1 token of 64/8 heads, 4 sequences of 1000..4000
+// keys 20.0 / 18.9 / 20.4 us, 1 of 3000 12.2 / 13.9 / 17.3, 16 of 300..1000 (32/8 heads)
+// 18.8 / 18.1 / 20.3; on tcgen05, 64/8 heads, 4 tokens of 2 sequences of 2000..4000 keys
+// 22.3 / 23.6 / 27.5, 5 of 1 of 6000 22.1 / 23.5 / 27.3, 5 of 16 of 300..1000 26.6 / 26.6 /
+// 18.9 (whole units then, without a merge).
 constexpr int32_t kMultiMinKeys = 256, kMultiTcMinKeys = 512;
 
 struct MultiWork {
@@ -660,8 +667,10 @@ __global__ void __launch_bounds__(MultiCfg<D, CF>::kThreads, MultiCfg<D, CF>::kC
 // unit merges it, over the partials of worker w - 1 and of those from w on until the
 // unit's end.
 // WIDE, for few units (grid.x) over many workers: a CTA per unit and row, whose warps
-// share the row's partials. 55 partials of 8 heads one after another took a warp 24
-// us, a third of the whole step over 131072 keys.
+// share the row's partials: at 55 workers a unit (1 sequence of 131072 keys, 64/8 heads,
+// e4m3) the step takes 50 us, against 70 by single warps, at 13.9 49 against 54, at 6.9
+// 51 either way; on tcgen05 at 18.5 37 against 42, at 9.3 55.5 against 59, at 4.6 95
+// against 93.
 constexpr int kMultiMergeWarps = 4, kMultiWideWarps = 8, kMultiWideParts = 8;
 
 template <int D, int KEYS, int MIN_CHUNKS, bool WIDE>

@@ -17,10 +17,12 @@
 //     their own maximum, sum and O.
 // The 2 RF states of a row are folded at a segment's end.
 //
-// Measured: 16 sequences of 1000..32768 keys, 5 tokens of 64/8 heads (40 rows): 187 us,
-// 6.2 TB/s, 0.94 of a copy's rate (under a power cap, at 1.45 GHz, 215 us: the chain
-// is then the longer side); 32 of 1024..8192, 8 tokens of 32/8 heads over e4m3: 124
-// us, 2.5 TB/s, bound by the converter and the chain.
+// Measured (kernels back to back in a graph, inputs larger than L2): 16 sequences of
+// 1000..32768 keys, 5 tokens of 64/8 heads (40 rows): 187 to 193 us, 6.0 to 6.2 TB/s,
+// 0.91 to 0.94 of a copy's rate (in runs of seconds the power cap lowers the clock to
+// 1.45 GHz and the chain is the longer side: 215 us); 32 of 1024..8192, 8 tokens of 32/8
+// heads: 110 us over bf16, 5.6 TB/s, 131 to 137 us over e4m3, 2.3 to 2.4 TB/s, bound by
+// the converter and the chain.
 //
 // Warps: 0-3 and 4-7 softmax of half t (thread = row = TMEM lane), 8 producer
 // (K; over an 8-bit cache K and V codes), 9 MMA issuer, 10-13 converter (V bf16

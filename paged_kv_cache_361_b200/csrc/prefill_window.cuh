@@ -23,12 +23,15 @@
 //   * O goes out as bf16, half as wide, through shared memory for every tile.
 // Grid (kv heads, sequences, pairs), the last (longest) pair first. One CTA per
 // SM that walks the pairs, the key ring running on from one to the next, was
-// slower (window of 1024: 340 against 297 us): its code outgrew the instruction
-// caches.
+// slower (window of 1024: 340 us where this form took 297; why was not found).
 //
-// Measured: two prompts of 3001 and 4096 tokens, 64/8 heads, window 1024: 308 us, 700
-// TFLOP/s; eight of 700..2048, 32/32 heads, cap 50: 279 us, 510 TFLOP/s. Bound by a
-// CTA's ends (5 us) and the chain of a chunk (1.1 us), not by a unit's rate.
+// Measured (launches back to back in a graph): two prompts of 3001 and 4096 tokens, 64/8
+// heads, window 1024: 281 us over bf16, 725 TFLOP/s, 297 over e4m3, 310 over int8; eight
+// of 700..2048, 32/32 heads, cap 50: 252 us, 567 TFLOP/s; with an L2 flush before each
+// launch 303 and 264 us. Bound by a CTA's ends (5 us) and the chain of a chunk (1.1 us),
+// not by a unit's rate. A chunk behind a long context has few CTAs, each of which walks
+// all its keys: 17 to 256 tokens of 64/8 heads behind 8192 keys 146 to 150 us, behind
+// 32768 549 to 567.
 //
 // Warps: 0-3 and 4-7 softmax of tile t (thread = row = TMEM lane), 8 producer
 // (bf16: K; 8-bit: K and V codes), 9 and 10 MMA of tile 0 and 1, 11-14 converter,
@@ -49,7 +52,7 @@ struct WindowArgs {
   __nv_bfloat16* out;      // [num_tokens][hq][D]
   float* lse;              // [num_tokens][hq] or null
   int64_t num_blocks;
-  int32_t num_seqs, num_tokens, max_q, hq, hkv, bs, max_blocks, max_ctx;
+  int32_t num_tokens, max_q, hq, hkv, bs, max_blocks, max_ctx;
   int32_t gshift, bshift;  // log2 of hq / hkv and of block_size
   int32_t window;          // >= 1; max_ctx or more: every earlier key
   ScoreScale score;
@@ -95,8 +98,9 @@ __global__ void __launch_bounds__(WindowCfg<D, CF>::kThreads, 1)
   constexpr int S = Cfg::kStages, C = Cfg::kChunk, CS = F8 ? Cfg::kCodeStages : 1;
   // A K stage is released by the softmax warps, which see S done, or with capped
   // scores, where they have the most to do, by a commit of the MMA warps (a commit
-  // waits behind the MMAs in the issue queue: window of 1024, 288 against 297 us;
-  // capped, 247 against 242)
+  // waits behind the MMAs in the issue queue: back to back, by the softmax warps and by
+  // a commit, window of 1024 288 and 297 us, capped 247 and 242, with weights not yet
+  // scaled)
   constexpr bool kSoftmaxFreesK = !CAPPED;
 
   extern __shared__ uint8_t smem_raw[];

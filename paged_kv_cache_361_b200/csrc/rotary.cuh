@@ -10,9 +10,10 @@
 // new K, V written at their block position.
 //
 // Bound by HBM: every input byte is read once and every output byte written
-// once, three operations per rotated element (16231 tokens of 32 / 32 heads in
-// bf16: 138 us, 5.85 TB/s, 0.89 of a copy's rate; 20011 of 64 / 8 heads into an e4m3
-// cache: 142 us, 5.54 TB/s). A thread owns one unit (16
+// once, three operations per rotated element (back to back: 16231 tokens of 32 / 32
+// heads in bf16 138 us, 5.9 TB/s, 0.89 of a copy's rate, in fp32 312 us, 5.1 TB/s, 0.78;
+// 20011 of 64 / 8 heads, half of each rotated, into an e4m3 cache 138 us, 5.7 TB/s, int8
+// 148 us, 5.3 TB/s). A thread owns one unit (16
 // elements) of several head rows of a token: its cosines, sines and offsets are
 // read and computed once for all of them. A unit is two 8-element pieces that
 // hold both members of its pairs: with halves paired, piece u and the piece
@@ -125,11 +126,11 @@ __device__ __forceinline__ void store_codes(uint8_t* p, const float2 (&f)[4], fl
 
 // T: input type; CF: 0 for a cache of the input type, kCodeE4M3 / kCodeS8 for
 // an 8-bit cache. The grid is at most the four CTAs that fit on every SM, walking
-// the tokens: a second wave would cost more than the walk (prompts of 16231
-// tokens, 32 / 32 heads: 146 us, against 167 us at one CTA per token). q rows and
-// k, v rows have loops of their own, fewer instructions for each (20011 tokens, 64 /
-// 8 heads over e4m3: 133 us, against 147 us in one loop). Three CTAs with the next
-// row's loads in flight were slower (150 us).
+// the tokens: a second wave would cost more than the walk. q rows and k, v rows have
+// loops of their own, fewer instructions for each. Side by side, each pair as the kernel
+// was at that step: prompts of 16231 tokens, 32 / 32 heads 146 us, 167 at one CTA per
+// token; 20011 tokens, 64 / 8 heads over e4m3 133 us, 147 in one loop, 150 with three CTAs
+// and the next row's loads in flight.
 template <typename T, int CF>
 __global__ void __launch_bounds__(256, 4) rotate_and_cache_kernel(const RotateArgs a) {
   const int32_t D = 16 << a.dshift;
