@@ -189,7 +189,8 @@ def pa_reshape_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
 
 def _on(t, name, dtype, ndim, device_index):
     """data_ptr of a contiguous tensor of that dtype and rank on the cache's device."""
-    if t.dtype is not dtype or t.get_device() != device_index or t.dim() != ndim or not t.is_contiguous():
+    if (not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device_index or t.dim() != ndim
+            or not t.is_contiguous()):
         _dev(t, name, dtype, ndim)
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{device_index}")
     return t.data_ptr()
@@ -224,8 +225,8 @@ def _stream_on(device_index, stream) -> int:
 def _token_rows(t: torch.Tensor, name: str, dtype, num_tokens, heads, head_dim, device_index) -> int:
     """Elements from one token's [heads][head_dim] row to the next, for a tensor
     whose rows are contiguous (a view of a wider projection's rows, say)."""
-    if t.dtype is not dtype or t.get_device() != device_index:
-        if not t.is_cuda:
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.get_device() != device_index:
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError(f"{name} must be a CUDA tensor")
         if t.dtype is not dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
@@ -246,6 +247,14 @@ def _token_rows(t: torch.Tensor, name: str, dtype, num_tokens, heads, head_dim, 
     return st
 
 
+def _tokens_heads(t, name: str) -> tuple[int, int]:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [num_tokens][heads][head_dim]")
+    return t.shape[0], t.shape[1]
+
+
 def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved=False,
                         stream=None):
     """Rotates q and k by their positions (int32) and cos_sin, fp32
@@ -254,16 +263,14 @@ def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     of one projection's rows; q and q_out may be None."""
     c = make_cache(k_cache, v_cache)
     dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
-    n = int(k.shape[0])
+    n = _tokens_heads(k, "k")[0]
     sk, sv = _token_rows(k, "k", dt, n, hkv, d, dev), _token_rows(v, "v", dt, n, hkv, d, dev)
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     sq = hq = 0
     qp = qo = None
     if q is not None:
-        if q.dim() != 3:
-            raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
-        hq = int(q.shape[1])
+        hq = _tokens_heads(q, "q")[1]
         sq, qp, qo = _token_rows(q, "q", dt, n, hq, d, dev), q.data_ptr(), _on(q_out, "q_out", dt, 3, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be [num_tokens][num_q_heads][head_dim]")
@@ -283,10 +290,7 @@ def check_rotate(q, k, v, cos_sin, k_cache, v_cache):
     """Raises what pa_rotate_and_cache would for these tensors."""
     c = make_cache(k_cache, v_cache)
     dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
-    n = int(k.shape[0])
-    if q.dim() != 3:
-        raise ValueError("q must be [num_tokens][num_q_heads][head_dim]")
-    hq = int(q.shape[1])
+    n, hq = _tokens_heads(k, "k")[0], _tokens_heads(q, "q")[1]
     sq, sk, sv = (_token_rows(t, name, dt, n, heads, d, dev)
                   for name, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)))
     _on(cos_sin, "cos_sin", torch.float32, 2, dev)

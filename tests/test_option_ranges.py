@@ -120,3 +120,26 @@ def test_caps_are_checked_before_they_are_rounded(host_calls, name, cap):
     with pytest.raises(B.PagedAttnError) as e:
         host_calls(name, softcap=cap)
     assert e.value.status == B.PA_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("name", BOTH)
+@pytest.mark.parametrize("key", ["q", "out", "block_tables", "context_lens", "sinks", "lse"])
+def test_what_is_no_tensor_is_a_type_error(host_calls, name, key):
+    import numpy as np
+    for value in ([1, 2], np.zeros(4, dtype=np.float32)) + (() if key in ("sinks", "lse") else (None,)):
+        with pytest.raises(TypeError, match=key):
+            host_calls(name, **{key: value})
+
+
+@pytest.mark.parametrize("key", ["q", "k", "v", "q_out", "positions", "slot_mapping", "cos_sin"])
+def test_what_is_no_tensor_is_a_type_error_of_the_rotation(host_calls, key):
+    import numpy as np
+    import torch
+    rows = lambda h: torch.zeros(3, h, 64, dtype=torch.bfloat16)
+    cache = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    args = dict(q=rows(4), k=rows(2), v=rows(2), positions=torch.zeros(3, dtype=torch.int32), cos_sin=torch.zeros(9, 64),
+                slot_mapping=torch.zeros(3, dtype=torch.int64), k_cache=cache, v_cache=cache.clone(), q_out=rows(4))
+    B.pa_rotate_and_cache(**args)
+    for value in ([1, 2], np.zeros((3, 2, 64), dtype=np.float32)) + (() if key in ("q", "q_out") else (None,)):
+        with pytest.raises(TypeError, match=key):
+            B.pa_rotate_and_cache(**dict(args, **{key: value}))
