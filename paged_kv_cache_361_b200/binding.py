@@ -255,12 +255,10 @@ def _tokens_heads(t, name: str) -> tuple[int, int]:
     return t.shape[0], t.shape[1]
 
 
-def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved=False,
-                        stream=None):
-    """Rotates q and k by their positions (int32) and cos_sin, fp32
-    [max_positions][rotary_dim] (see rotary_table), writes k and v to their
-    slots and q to q_out. q, k, v: [num_tokens][heads][head_dim], also as views
-    of one projection's rows; q and q_out may be None."""
+def prepare_rotate(q, k, v, cos_sin, k_cache, v_cache, q_out, interleaved=False, check=False):
+    """pa_rotate_and_cache of these tensors, checked, as a function of (positions,
+    slot_mapping, stream=None). With `check` the native call's own checks are made
+    now too, so that it can be refused before anything else is done."""
     c = make_cache(k_cache, v_cache)
     dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
     n = _tokens_heads(k, "k")[0]
@@ -274,32 +272,36 @@ def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
         sq, qp, qo = _token_rows(q, "q", dt, n, hq, d, dev), q.data_ptr(), _on(q_out, "q_out", dt, 3, dev)
         if q_out.shape != q.shape:
             raise ValueError("q_out must be [num_tokens][num_q_heads][head_dim]")
-    table = _on(cos_sin, "cos_sin", torch.float32, 2, dev)
-    pos, slots = _on(positions, "positions", torch.int32, 1, dev), _on(slot_mapping, "slot_mapping", torch.int64, 1, dev)
-    if positions.shape[0] != n or slot_mapping.shape[0] != n:
-        raise ValueError("positions and slot_mapping must have an entry for every token of k")
+    table, kp, vp = _on(cos_sin, "cos_sin", torch.float32, 2, dev), k.data_ptr(), v.data_ptr()
     if v_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be on one device")
     max_positions, rotary_dim = cos_sin.shape
-    _call_on(dev, _lib().pa_rotate_and_cache, "pa_rotate_and_cache", qp, sq, k.data_ptr(), sk, v.data_ptr(), sv, pos,
-             table, max_positions, rotary_dim, 1 if interleaved else 0, slots, n, hq, ctypes.byref(c), qo,
-             _stream_on(dev, stream))
+    turn, fn = 1 if interleaved else 0, _lib().pa_rotate_and_cache
+    if check:
+        # the call without tokens checks all but the pointers, and uses none
+        _check(fn(16, sq, 16, sk, 16, sv, None, None, max(1, max_positions), rotary_dim, turn, None, 0, hq,
+                  ctypes.byref(c), 32, None), "pa_rotate_and_cache")
+        if n and ((qp or 0) | (qo or 0) | kp | vp | table) % 16:
+            raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
+
+    def call(positions, slot_mapping, stream=None):
+        pos = _on(positions, "positions", torch.int32, 1, dev)
+        slots = _on(slot_mapping, "slot_mapping", torch.int64, 1, dev)
+        if positions.shape[0] != n or slot_mapping.shape[0] != n:
+            raise ValueError("positions and slot_mapping must have an entry for every token of k")
+        _call_on(dev, fn, "pa_rotate_and_cache", qp, sq, kp, sk, vp, sv, pos, table, max_positions, rotary_dim, turn, slots,
+                 n, hq, ctypes.byref(c), qo, _stream_on(dev, stream))
+    call.tensors = (q, k, v, cos_sin, k_cache, v_cache, q_out)  # alive as long as their addresses
+    return call
 
 
-def check_rotate(q, k, v, cos_sin, k_cache, v_cache):
-    """Raises what pa_rotate_and_cache would for these tensors."""
-    c = make_cache(k_cache, v_cache)
-    dt, hkv, d, dev = input_dtype(k_cache.dtype), c.num_kv_heads, c.head_dim, k_cache.get_device()
-    n, hq = _tokens_heads(k, "k")[0], _tokens_heads(q, "q")[1]
-    sq, sk, sv = (_token_rows(t, name, dt, n, heads, d, dev)
-                  for name, t, heads in (("q", q, hq), ("k", k, hkv), ("v", v, hkv)))
-    _on(cos_sin, "cos_sin", torch.float32, 2, dev)
-    max_positions, rotary_dim = cos_sin.shape
-    # the call without tokens: it checks all but the pointers, and uses none
-    _check(_lib().pa_rotate_and_cache(16, sq, 16, sk, 16, sv, None, None, max(1, max_positions), rotary_dim, 0, None, 0, hq,
-                                      ctypes.byref(c), 32, None), "pa_rotate_and_cache")
-    if n and any(t.data_ptr() % 16 for t in (q, k, v, cos_sin)):
-        raise PagedAttnError(PA_ERR_INVALID_ARG, "pa_rotate_and_cache")
+def pa_rotate_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_out, interleaved=False,
+                        stream=None):
+    """Rotates q and k by their positions (int32) and cos_sin, fp32
+    [max_positions][rotary_dim] (see rotary_table), writes k and v to their
+    slots and q to q_out. q, k, v: [num_tokens][heads][head_dim], also as views
+    of one projection's rows; q and q_out may be None."""
+    prepare_rotate(q, k, v, cos_sin, k_cache, v_cache, q_out, interleaved)(positions, slot_mapping, stream)
 
 
 def rotary_table(max_positions: int, rotary_dim: int, base: float = 10000.0, device="cuda") -> torch.Tensor:

@@ -38,17 +38,25 @@ class _Staging:
         h.numpy()[...] = arr
         return h.to(self.device, non_blocking=True)
 
-    def reserve(self, *shape):
-        """An upload of at most that shape whose memory is taken now: a function of
-        the array that returns its rows on the device, for once."""
-        h = torch.empty(shape, dtype=self.t_dtype, pin_memory=True)
-        d = torch.empty(shape, dtype=self.t_dtype, device=self.device)
 
-        def send(arr: np.ndarray) -> torch.Tensor:
-            n = len(arr)
-            h.numpy()[:n] = arr
-            return d[:n].copy_(h[:n], non_blocking=True)
-        return send
+class _AppendUpload:
+    """Slots, block pairs and positions of one append, uploaded in one copy; the memory
+    is taken at the start, before the block manager changes."""
+
+    def __init__(self, tokens: int, max_pairs: int, device):
+        self.at = (8 * tokens, 8 * (tokens + max_pairs), 8 * (tokens + max_pairs) + 4 * tokens)
+        self.host = torch.empty(self.at[2], dtype=torch.uint8, pin_memory=True)
+        self.dev = torch.empty(self.at[2], dtype=torch.uint8, device=device)
+
+    def send(self, slots: np.ndarray, pairs: np.ndarray, pos: np.ndarray):
+        """The three on the device: int64 [tokens], int32 [len(pairs)][2], int32 [tokens]."""
+        a, b, _ = self.at
+        h = self.host.numpy()
+        h[:a].view(np.int64)[:] = slots
+        h[a:a + 8 * len(pairs)].view(np.int32)[:] = pairs.reshape(-1)
+        h[b:].view(np.int32)[:] = pos
+        d = self.dev.copy_(self.host, non_blocking=True)
+        return d[:a].view(torch.int64), d[a:a + 8 * len(pairs)].view(torch.int32).view(-1, 2), d[b:].view(torch.int32)
 
 
 class PagedKVCache:
@@ -172,18 +180,19 @@ class PagedKVCache:
             raise ValueError("a sequence outgrew the rotary table")
         # whatever may be refused or find no memory comes before anything changes: only
         # copies and launches follow _extend
-        B.check_rotate(q, k, v, cos_sin, self.k_cache, self.v_cache)
         q_out = torch.empty(q.shape, dtype=q.dtype, device=self.device)
+        rotate = B.prepare_rotate(q, k, v, cos_sin, self.k_cache, self.v_cache, q_out, interleaved, check=True)
         T = sum(counts)
         if T == 0:
             self._extend(seq_ids, counts)
             return q_out
-        pos = self._lens.upload(np.concatenate([np.arange(f, f + c, dtype=np.int32) for f, c in zip(first, counts)]))
-        send_slots, send_pairs = self._slots.reserve(T), self._pairs.reserve(len(seq_ids), 2)
+        pos = np.concatenate([np.arange(f, f + c, dtype=np.int32) for f, c in zip(first, counts)])
+        upload = _AppendUpload(T, len(seq_ids), self.device)
         slots, pairs = self._extend(seq_ids, counts)
+        slots_d, pairs_d, pos_d = upload.send(slots, pairs, pos)
         if len(pairs):
-            B.pa_copy_blocks(self.k_cache, self.v_cache, send_pairs(pairs))
-        B.pa_rotate_and_cache(q, k, v, pos, cos_sin, send_slots(slots), self.k_cache, self.v_cache, q_out, interleaved)
+            B.pa_copy_blocks(self.k_cache, self.v_cache, pairs_d)
+        rotate(pos_d, slots_d)
         return q_out
 
     def enable_swap(self, num_host_blocks: int):
