@@ -51,35 +51,37 @@ _PF = ["common.cuh", "decode_common.cuh", "decode_f8.cuh", "prefill_mma.cuh", "p
        "capi.cu"]
 NCU_TRAFFIC: dict = {
     ("llama2_7b_mha", "bfloat16", 0, "decode"): dict(
-        bytes=1_079_387_221 + 2_192_299, files=_DEC + ["decode_simt.cuh"], sha="8e318919c2abc840",
+        bytes=1_079_315_541 + 2_209_792, files=_DEC + ["decode_simt.cuh"], sha="cf39d3c561374b87",
         note="decode_simt_kernel of pa_decode_append (the step's only launch), 3 launches"),
     ("llama2_7b_mha", "float8_e4m3fn", 0, "decode"): dict(
-        bytes=540_502_443 + 1_836_459, files=_DEC + ["decode_f8.cuh"], sha="5ff75b7b610d5d43",
+        bytes=540_510_805 + 2_370_560, files=_DEC + ["decode_f8.cuh"], sha="c28535dec301a8c2",
         note="decode_f8_kernel (e4m3) of pa_decode_append, 3 launches"),
     ("llama2_7b_mha", "int8", 0, "decode"): dict(
-        bytes=540_523_947 + 1_852_928, files=_DEC + ["decode_f8.cuh"], sha="5ff75b7b610d5d43",
+        bytes=540_487_936 + 1_882_709, files=_DEC + ["decode_f8.cuh"], sha="c28535dec301a8c2",
         note="decode_f8_kernel (int8) of pa_decode_append, 3 launches"),
     ("long_context_split", "bfloat16", 512, "decode"): dict(
-        bytes=1_343_030_613 + 6_136_832 + 21_471_744, files=_DEC + ["decode_mma.cuh"], sha="572fd0d77d91b599",
+        bytes=1_343_085_312 + 6_101_248 + 21_471_403, files=_DEC + ["decode_mma.cuh"], sha="f0fba0cac771f7a8",
         note="decode_mma_persistent_kernel + decode_reduce_kernel, 3 launches each"),
     ("parallel_sampling", "bfloat16", 0, "decode"): dict(
-        bytes=113_622_400 + 601_728, files=_DEC + ["decode_mma.cuh"], sha="572fd0d77d91b599",
+        bytes=113_651_072 + 359_552, files=_DEC + ["decode_mma.cuh"], sha="f0fba0cac771f7a8",
         note="decode_mma_kernel of pa_decode_append, 6 launches (1.17x the 97.5 MB of distinct blocks: with the "
              "longest-first order a prompt's samples no longer all run at once)"),
     ("parallel_sampling", "bfloat16", 0, "cascade"): dict(
-        bytes=32_022_272 + 768 + 72_888_013 + 103_168, files=_DEC + ["decode_mma.cuh", "prefill_mma.cuh"], sha="de27b89ffdac9c43",
+        bytes=32_022_699 + 811 + 72_883_814 + 100_813, files=_DEC + ["decode_mma.cuh", "prefill_mma.cuh"],
+        sha="37e79aa7f7b3db5b",
         note="prefill_mma_kernel (prefix pass) + decode_mma_kernel (suffixes and fold), 5-6 launches each"),
     ("continuous_batching", "bfloat16", 0, "decode"): dict(
-        bytes=835_087_625 + 2_439_945, files=_DEC + ["decode_mma.cuh"], sha="572fd0d77d91b599",
+        bytes=835_067_341 + 2_510_942, files=_DEC + ["decode_mma.cuh"], sha="f0fba0cac771f7a8",
         note="decode_mma_kernel of pa_decode_append over steps 0-29 of the trace (32768-block pool); their "
              "algorithmic mean is 825.0 MB per step (x1.015), the 200-step mean 811.2 MB"),
     ("prefill_llama2_7b_mha", "bfloat16", 0, "prefill"): dict(
-        bytes=1_308_881_000 + 228_545_280, files=_PF, sha="de28dba00f317626",
-        how="ncu capture (the profile's metric set, one launch)", note="prefill_tc_kernel, 1 launch (Q, K/V per tile pair not served by L2, the fp32 output)"),
+        bytes=1_310_775_954 + 225_563_099, files=_PF, sha="9380b81bcd2728dd",
+        note="prefill_tc_kernel, 7 launches (Q, K/V per tile pair not served by L2, the fp32 output)"),
     ("prefill_llama2_7b_mha", "float8_e4m3fn", 0, "prefill"): dict(
-        bytes=662_598_656 + 226_810_368, files=_PF, sha="de28dba00f317626", how="ncu capture (the profile's metric set, one launch)", note="prefill_tc_kernel (e4m3), 1 launch"),
+        bytes=661_598_098 + 223_392_987, files=_PF, sha="9380b81bcd2728dd",
+        note="prefill_tc_kernel (e4m3), 7 launches"),
     ("prefill_gqa8", "bfloat16", 0, "prefill"): dict(
-        bytes=758_603_264 + 483_280_640, files=_PF, sha="de28dba00f317626", how="ncu capture (the profile's metric set, one launch)", note="prefill_tc_kernel, 1 launch"),
+        bytes=714_315_191 + 481_272_137, files=_PF, sha="9380b81bcd2728dd", note="prefill_tc_kernel, 7 launches"),
 }
 CSRC = os.path.join(ROOT, "paged_kv_cache_361_b200", "csrc")
 

@@ -419,13 +419,15 @@ typedef struct {
  * rounded once to bf16. Over an 8-bit cache q and the weights enter the products
  * as f16 (|q| up to 65504). With max_q_len * num_q_heads / num_kv_heads above 8 the
  * weights are f16 over a bf16 cache too, and so is V: |V| up to 65504, values
- * below 2^-14 to a multiple of 2^-24. A weight as f16 keeps 11 bits down to 2^-21
+ * below 2^-14 to a multiple of 2^-24. (The form is the call's, by max_q_len: within
+ * these bounds a sequence's result depends on what it is batched with.) A weight as f16 keeps 11 bits down to 2^-21
  * of its row's largest; below, it is off by at most 2^-32 of the largest: n keys
  * move the result by at most n 2^-32 max|V|. V must be finite at every key that some
  * new token of its sequence sees (a weight of 0 does not hide an infinity or NaN
  * there). Supported: bf16, e4m3 or int8 cache, block_size 8, 16 or 32, head_dim
  * 64 or 128, num_q_heads / num_kv_heads in {1, 2, 4, 8}, max_context_len up to
- * 2^30. Calls sharing a workspace must not overlap on the GPU. options may be
+ * 2^30. A query of NaN gives a row of NaN. The same call gives the same bits,
+ * whatever the pool holds where no row looks. Calls sharing a workspace must not overlap on the GPU. options may be
  * NULL: plain causal attention.
  */
 pa_status pa_decode_multi(const void* q, int32_t num_tokens, int32_t num_seqs, const int32_t* cu_q_lens,
